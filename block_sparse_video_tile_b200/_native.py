@@ -22,7 +22,9 @@ DEVERR = {0: "none", 1: "wait timeout", 2: "tile index out of range", 3: "kept l
 EXPORTS = ("vsa_tile_count", "vsa_kv_tile_count", "vsa_topk_from_sparsity", "vsa_select_workspace_bytes",
            "vsa_select", "vsa_select_noalloc", "vsa_attn_fwd", "vsa_select_coarse_workspace_bytes",
            "vsa_select_coarse", "vsa_attn_fwd_gated", "vsa_forward_host_workspace_bytes", "vsa_forward_host",
-           "vsa_device_error", "vsa_status_string")
+           "vsa_qk_norm_rope", "vsa_qk_norm_rope_bwd_workspace_bytes", "vsa_qk_norm_rope_bwd",
+           "vsa_window_attn_workspace_bytes", "vsa_window_attn", "vsa_window_attn_bwd_workspace_bytes",
+           "vsa_window_attn_bwd", "vsa_device_error", "vsa_status_string")
 SELECT_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
 
@@ -34,6 +36,29 @@ class VsaShape(ctypes.Structure):
     """vsa_shape: zero key/value fields mean "the query grid / tile"."""
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "H", "T", "Hh", "W", "d", "tt", "th", "tw", "dtype", "layout",
                                               "Tk", "Hk", "Wk", "tk", "hk", "wk", "prefix_tiles")]
+
+
+_S3 = ctypes.c_int64 * 3
+
+
+class VsaQkSide(ctypes.Structure):
+    """vsa_qk_side: queries or keys of vsa_qk_norm_rope."""
+    _fields_ = ([(n, ctypes.c_int32) for n in ("B", "H", "T", "Hh", "W", "weight_f32")] +
+                [("x", ctypes.c_void_p), ("x_s", _S3), ("y", ctypes.c_void_p), ("y_s", _S3), ("dx", ctypes.c_void_p),
+                 ("dx_s", _S3)] + [(n, ctypes.c_void_p) for n in ("weight", "table", "dweight")])
+
+
+class VsaNormRope(ctypes.Structure):
+    """vsa_norm_rope: what both sides share."""
+    _fields_ = [("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("split", ctypes.c_int32 * 3), ("eps", ctypes.c_float)]
+
+
+class VsaWindow(ctypes.Structure):
+    """vsa_window: extents, units and strides of a window attention."""
+    _fields_ = ([(n, ctypes.c_int32) for n in ("B", "Hq", "Hkv", "Nq", "Nk", "d", "dtype", "window", "sink", "unit")] +
+                [("kv_len", ctypes.c_void_p), ("q_start", ctypes.c_void_p)] +
+                [(n + "_s", _S3) for n in ("q", "k", "v", "o", "do", "dq", "dk", "dv")])
 
 
 class VsaError(RuntimeError):
@@ -79,6 +104,21 @@ def lib() -> ctypes.CDLL:
         L.vsa_forward_host_workspace_bytes.restype = SZ
         L.vsa_forward_host.argtypes = [S, P, P, P, I32, ctypes.c_float, P, P, P, I32, P, SZ, P]
         L.vsa_forward_host.restype = ctypes.c_int
+        NR, QS, WN = (ctypes.POINTER(t) for t in (VsaNormRope, VsaQkSide, VsaWindow))
+        L.vsa_qk_norm_rope.argtypes = [NR, QS, QS, P]
+        L.vsa_qk_norm_rope.restype = ctypes.c_int
+        L.vsa_qk_norm_rope_bwd_workspace_bytes.argtypes = [NR, QS, QS]
+        L.vsa_qk_norm_rope_bwd_workspace_bytes.restype = SZ
+        L.vsa_qk_norm_rope_bwd.argtypes = [NR, QS, QS, P, SZ, P]
+        L.vsa_qk_norm_rope_bwd.restype = ctypes.c_int
+        L.vsa_window_attn_workspace_bytes.argtypes = [WN]
+        L.vsa_window_attn_workspace_bytes.restype = SZ
+        L.vsa_window_attn.argtypes = [WN, P, P, P, ctypes.c_float, P, P, P, SZ, P]
+        L.vsa_window_attn.restype = ctypes.c_int
+        L.vsa_window_attn_bwd_workspace_bytes.argtypes = [WN]
+        L.vsa_window_attn_bwd_workspace_bytes.restype = SZ
+        L.vsa_window_attn_bwd.argtypes = [WN, P, P, P, P, P, P, ctypes.c_float, P, P, P, P, SZ, P]
+        L.vsa_window_attn_bwd.restype = ctypes.c_int
         L.vsa_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint32), I32]
         L.vsa_device_error.restype = ctypes.c_int
         L.vsa_status_string.argtypes = [I32]

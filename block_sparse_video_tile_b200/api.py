@@ -15,9 +15,12 @@ import math
 import torch
 
 from ._native import DTYPE_BF16, DTYPE_F16, LAYOUT_BHND, LAYOUT_BNHD, VsaShape, check, lib
+from .norm_rope import qk_norm_rope, qk_norm_rope_bwd, rope_split, rope_table
+from .window import window_attn, window_attn_bwd
 
 __all__ = ["make_shape", "tile_count", "kv_tile_count", "topk_from_sparsity", "select", "select_coarse", "attn_fwd",
-           "forward", "forward_host", "device_error", "select_workspace_bytes", "select_coarse_workspace_bytes"]
+           "forward", "forward_host", "device_error", "select_workspace_bytes", "select_coarse_workspace_bytes",
+           "rope_split", "rope_table", "qk_norm_rope", "qk_norm_rope_bwd", "window_attn", "window_attn_bwd"]
 
 
 _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
@@ -193,15 +196,21 @@ def attn_fwd(q, k, v, idx, grid, tile, *, grid_k=None, tile_k=None, layout: str 
 
 
 def forward(q, k, v, grid, tile, topk: int | None = None, *, sparsity: float | None = None, grid_k=None,
-            tile_k=None, layout: str = "bhnd", prefix_tiles: int = 0, scale=None, gate=None, stream=None):
+            tile_k=None, layout: str = "bhnd", prefix_tiles: int = 0, scale=None, gate=None, norm_rope=None,
+            stream=None):
     """select + attn_fwd: (O, LSE, idx).  Give topk, or sparsity (the fraction
     of key/value tiles left out, as in the fastbsa page's "Use" example).
-    With gate (like q), O also carries the gated pooled coarse branch."""
+    With gate (like q), O also carries the gated pooled coarse branch.  With
+    norm_rope (keyword arguments of qk_norm_rope: table, table_k, q_weight,
+    k_weight, eps, split, interleaved), q and k are the projections' rows and
+    go through qk_norm_rope first."""
     if (topk is None) == (sparsity is None):
         raise ValueError("give exactly one of topk and sparsity")
     if topk is None:
         topk = topk_from_sparsity(grid, tile, sparsity, grid_k, tile_k, _dims(q, layout)[3], prefix_tiles)
     kw = dict(grid_k=grid_k, tile_k=tile_k, layout=layout, stream=stream)
+    if norm_rope is not None:
+        q, k = qk_norm_rope(q, k, grid, grid_k=grid_k, layout=layout, stream=stream, **norm_rope)
     if gate is None:
         idx = select(q, k, grid, tile, topk, prefix_tiles=prefix_tiles, **kw)
         o, lse = attn_fwd(q, k, v, idx, grid, tile, scale=scale, **kw)

@@ -1,6 +1,7 @@
 // libvsa.cu -- the C ABI (declared in include/vsa.h): argument checks, tile
-// geometry, TMA descriptor encoding and kernel launches.  The only translation
-// unit of libvsa.so; the kernels live in the headers it includes.
+// geometry, TMA descriptor encoding and kernel launches of the block-sparse
+// calls (norm_rope.cu and window.cu hold the other two units of libvsa.so); the
+// kernels live in the headers it includes.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -14,6 +15,7 @@
 #include "attn_kernel.cuh"
 #include "select_kernels.cuh"
 #include "tma_encode.cuh"
+#include "vsa_host.h"
 #include "vsa_geometry.cuh"
 
 namespace vsa {
@@ -79,7 +81,7 @@ static int make_geoms(const vsa_shape* s, Geom* gq, Geom* gk) {
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-static int check_arch() {
+int check_arch() {
   static int cached[kMaxDevices];          // 0 unknown, 1 ok, 2 bad
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return VSA_ERR_CUDA;
@@ -147,7 +149,7 @@ static int symbol_address(const void* symbol, SymbolCache& c, void** out) {
   return VSA_OK;
 }
 
-static unsigned int* device_error_ptr() {
+unsigned int* device_error_ptr() {
   static SymbolCache cache;
   void* p = nullptr;
   return symbol_address(&g_device_error, cache, &p) == VSA_OK ? static_cast<unsigned int*>(p) : nullptr;

@@ -1,0 +1,141 @@
+// window.cu -- vsa_window_attn and its gradient: argument checks and launches
+// (declared in include/vsa.h).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "vsa.h"
+#include "vsa_host.h"
+#include "window_args.cuh"
+#include "window_simple.cuh"
+
+namespace vsa {
+
+static int win_args(const vsa_window* w, float scale, WinArgs* a) {
+  if (w == nullptr) return VSA_ERR_INVALID_ARG;
+  if (w->B <= 0 || w->Hq <= 0 || w->Hkv <= 0 || w->Nq <= 0 || w->Nk <= 0) return VSA_ERR_INVALID_ARG;
+  if (w->Hq % w->Hkv != 0 || w->window < 1 || w->sink < 0 || w->unit < 1) return VSA_ERR_INVALID_ARG;
+  if (w->d != 64 && w->d != 128) return VSA_ERR_UNSUPPORTED;
+  if (w->dtype != VSA_DTYPE_BF16 && w->dtype != VSA_DTYPE_F16) return VSA_ERR_UNSUPPORTED;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return VSA_ERR_INVALID_ARG;
+  if (!aligned_to(w->kv_len, 4) || !aligned_to(w->q_start, 4)) return VSA_ERR_ALIGNMENT;
+  if (w->Nq > kWinMaxPos || w->Nk > kWinMaxPos || w->B > 65535 || w->Hq > 65535) return VSA_ERR_TOO_LARGE;
+  a->B = w->B; a->Hq = w->Hq; a->Hkv = w->Hkv; a->group = w->Hq / w->Hkv;
+  a->Nq = w->Nq; a->Nk = w->Nk;
+  a->unit = w->unit;
+  a->window = w->window;
+  a->sink_tok = 1ll * w->sink * w->unit;
+  a->kv_len = w->kv_len;
+  a->q_start = w->q_start;
+  a->scale = scale;
+  a->scale_log2 = scale * 1.4426950408889634f;
+  int rc;
+  if ((rc = take_strides(w->q_s, w->B, w->Nq, w->Hq, w->d, a->qs)) != VSA_OK ||
+      (rc = take_strides(w->k_s, w->B, w->Nk, w->Hkv, w->d, a->ks)) != VSA_OK ||
+      (rc = take_strides(w->v_s, w->B, w->Nk, w->Hkv, w->d, a->vs)) != VSA_OK ||
+      (rc = take_strides(w->o_s, w->B, w->Nq, w->Hq, w->d, a->os)) != VSA_OK)
+    return rc;
+  return VSA_OK;
+}
+
+static int win_bwd_strides(const vsa_window* w, WinArgs* a) {
+  int rc;
+  if ((rc = take_strides(w->do_s, w->B, w->Nq, w->Hq, w->d, a->dos)) != VSA_OK ||
+      (rc = take_strides(w->dq_s, w->B, w->Nq, w->Hq, w->d, a->dqs)) != VSA_OK ||
+      (rc = take_strides(w->dk_s, w->B, w->Nk, w->Hkv, w->d, a->dks)) != VSA_OK ||
+      (rc = take_strides(w->dv_s, w->B, w->Nk, w->Hkv, w->d, a->dvs)) != VSA_OK)
+    return rc;
+  return VSA_OK;
+}
+
+static size_t win_bwd_bytes(const vsa_window* w) {
+  return (static_cast<size_t>(w->B) * w->Hq * w->Nq * sizeof(float) + 255) & ~static_cast<size_t>(255);
+}
+
+}  // namespace vsa
+
+using namespace vsa;
+
+extern "C" {
+
+size_t vsa_window_attn_workspace_bytes(const vsa_window* w) {
+  WinArgs a;
+  if (win_args(w, 1.f, &a) != VSA_OK) return 0;
+  return 0;
+}
+
+int vsa_window_attn(const vsa_window* w, const void* q, const void* k, const void* v, float softmax_scale, void* o,
+                    float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  WinArgs a;
+  int rc = win_args(w, softmax_scale, &a);
+  if (rc != VSA_OK) return rc;
+  if (q == nullptr || k == nullptr || v == nullptr || o == nullptr || lse == nullptr) return VSA_ERR_INVALID_ARG;
+  if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(o, 16) || !aligned_to(lse, 4) ||
+      !aligned_to(workspace, 16))
+    return VSA_ERR_ALIGNMENT;
+  if ((rc = check_arch()) != VSA_OK) return rc;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.out = static_cast<uint16_t*>(o);
+  a.lse = lse;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const dim3 grid((a.Nq + 7) / 8, a.Hq, a.B);
+  const bool f16 = w->dtype == VSA_DTYPE_F16;
+  if (w->d == 128) {
+    if (f16) window_fwd_simple<128, true><<<grid, 256, 0, st>>>(a);
+    else window_fwd_simple<128, false><<<grid, 256, 0, st>>>(a);
+  } else {
+    if (f16) window_fwd_simple<64, true><<<grid, 256, 0, st>>>(a);
+    else window_fwd_simple<64, false><<<grid, 256, 0, st>>>(a);
+  }
+  return cudaGetLastError() == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
+}
+
+size_t vsa_window_attn_bwd_workspace_bytes(const vsa_window* w) {
+  WinArgs a;
+  if (win_args(w, 1.f, &a) != VSA_OK || win_bwd_strides(w, &a) != VSA_OK) return 0;
+  return win_bwd_bytes(w);
+}
+
+int vsa_window_attn_bwd(const vsa_window* w, const void* d_o, const void* q, const void* k, const void* v,
+                        const void* o, const float* lse, float softmax_scale, void* dq, void* dk, void* dv,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  WinArgs a;
+  int rc = win_args(w, softmax_scale, &a);
+  if (rc != VSA_OK || (rc = win_bwd_strides(w, &a)) != VSA_OK) return rc;
+  const void* ptrs[] = {d_o, q, k, v, o, dq, dk, dv};
+  for (const void* p : ptrs)
+    if (p == nullptr) return VSA_ERR_INVALID_ARG;
+  if (lse == nullptr) return VSA_ERR_INVALID_ARG;
+  for (const void* p : ptrs)
+    if (!aligned_to(p, 16)) return VSA_ERR_ALIGNMENT;
+  if (!aligned_to(lse, 4) || !aligned_to(workspace, 16)) return VSA_ERR_ALIGNMENT;
+  if (workspace == nullptr || workspace_bytes < win_bwd_bytes(w)) return VSA_ERR_WORKSPACE;
+  if ((rc = check_arch()) != VSA_OK) return rc;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.o = static_cast<const uint16_t*>(o);
+  a.d_o = static_cast<const uint16_t*>(d_o);
+  a.lse = const_cast<float*>(lse);
+  a.dq = static_cast<uint16_t*>(dq);
+  a.dk = static_cast<uint16_t*>(dk);
+  a.dv = static_cast<uint16_t*>(dv);
+  a.delta = static_cast<float*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const dim3 gq((a.Nq + 7) / 8, a.Hq, a.B), gk((a.Nk + 7) / 8, a.Hkv, a.B);
+  const bool f16 = w->dtype == VSA_DTYPE_F16;
+#define VSA_WIN_BWD(D, F)                          \
+  do {                                             \
+    window_dq_simple<D, F><<<gq, 256, 0, st>>>(a); \
+    window_dkv_simple<D, F><<<gk, 256, 0, st>>>(a); \
+  } while (0)
+  if (w->d == 128) { if (f16) VSA_WIN_BWD(128, true); else VSA_WIN_BWD(128, false); }
+  else { if (f16) VSA_WIN_BWD(64, true); else VSA_WIN_BWD(64, false); }
+#undef VSA_WIN_BWD
+  return cudaGetLastError() == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -274,6 +274,105 @@ int vsa_forward_host(const vsa_shape* shape, const void* q, const void* k, const
                      float softmax_scale, void* o, float* lse, int32_t* idx, int32_t chunk_heads,
                      void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * What a video transformer's layer does to q and k before its attention, and
+ * attention over a sliding window (streaming and frame-causal generation).
+ * No page describes these calls; they are additions of this library.  They
+ * take tensors by strides: element (b, n, h, c) of a tensor is at
+ * ptr + b * s[0] + n * s[1] + h * s[2] + c elements, so both layouts, views
+ * of a fused projection and caches with room to grow need no copy.  Strides
+ * are multiples of 8 elements (16 bytes) and pointers 16-byte aligned
+ * (VSA_ERR_ALIGNMENT); the stride of an extent of 1 is not looked at, any
+ * other is positive (VSA_ERR_INVALID_ARG).  Outputs overlap neither each
+ * other nor an input.
+ * ------------------------------------------------------------------------ */
+
+/* One side (queries or keys) of vsa_qk_norm_rope. */
+typedef struct vsa_qk_side {
+  int32_t B, H;            /* batch, heads of this side                       */
+  int32_t T, Hh, W;        /* its grid: N = T * Hh * W tokens in raster order */
+  int32_t weight_f32;      /* weight's type: 0 the tensors', 1 float32        */
+  const void* x;           /* the projection's rows                           */
+  int64_t x_s[3];
+  void* y;                 /* forward: the result; backward: its gradient     */
+  int64_t y_s[3];
+  void* dx;                /* backward: the gradient of x (else NULL)         */
+  int64_t dx_s[3];
+  const void* weight;      /* [d], or NULL: ones                              */
+  const float* table;      /* rotation (below), or NULL: none                 */
+  float* dweight;          /* backward: float32 [d]; NULL with weight NULL    */
+} vsa_qk_side;
+
+/* Shared by both sides.  split: channels rotated by t, y and x, even, >= 0,
+ * sum d.  Channel pair p (0 .. d/2) is channels (2p, 2p+1) with interleaved,
+ * else (p, p + d/2); pairs 0 .. split[0]/2-1 turn with the token's t, the
+ * next split[1]/2 with its y, the rest with its x.  table: float32 cos and
+ * sin, [T * split[0]/2 + Hh * split[1]/2 + W * split[2]/2, 2]: T rows of the
+ * t pairs, then Hh rows of the y pairs, then W rows of the x pairs; 8-byte
+ * aligned. */
+typedef struct vsa_norm_rope {
+  int32_t d, dtype;        /* 64 or 128; VSA_DTYPE_*                          */
+  int32_t interleaved;
+  int32_t split[3];
+  float eps;               /* >= 0 and finite                                 */
+} vsa_norm_rope;
+
+/* For every row x of every token and head of both sides (k may be NULL):
+ *   u = x / sqrt(mean(x^2) + eps),  y = R(position) (weight * u)
+ * computed in float32 and rounded once.  One kernel launch. */
+int vsa_qk_norm_rope(const vsa_norm_rope* p, const vsa_qk_side* q, const vsa_qk_side* k, void* stream);
+
+/* Its gradient: from dy (in y) and x, dx and dweight,
+ *   g = R^T dy,  dweight = sum g * u,  h = g * weight,
+ *   dx = (h - u mean(h * u)) / sqrt(mean(x^2) + eps)
+ * dweight is summed in a fixed order (the same bits each time).
+ * workspace: at least vsa_qk_norm_rope_bwd_workspace_bytes bytes, 16-byte
+ * aligned (0: no weight asks for a gradient, workspace may be NULL).  One
+ * kernel launch, two with a weight. */
+size_t vsa_qk_norm_rope_bwd_workspace_bytes(const vsa_norm_rope* p, const vsa_qk_side* q, const vsa_qk_side* k);
+int vsa_qk_norm_rope_bwd(const vsa_norm_rope* p, const vsa_qk_side* q, const vsa_qk_side* k, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Attention over a sliding window of units, with the first units kept.
+ * A unit is `unit` consecutive tokens (a latent frame, Hh * W; or 1).  Query
+ * i of sequence b stands at position p = q_start[b] + i, key j at position j;
+ * p sees j if 0 <= p, j < kv_len[b], j/unit <= p/unit, and either
+ * p/unit - j/unit < window or j/unit < sink.  So the tokens of a unit see
+ * each other, the window - 1 units before theirs, and the first `sink`
+ * units.  A query that sees nothing gets O = 0 and LSE = -inf.
+ * Query head h reads key/value head h / (Hq / Hkv). */
+typedef struct vsa_window {
+  int32_t B, Hq, Hkv;      /* Hq a multiple of Hkv                            */
+  int32_t Nq, Nk;          /* queries per sequence; key/value rows held       */
+  int32_t d, dtype;        /* 64 or 128; VSA_DTYPE_*                          */
+  int32_t window, sink;    /* units: window >= 1, sink >= 0                   */
+  int32_t unit;            /* tokens, >= 1                                    */
+  const int32_t* kv_len;   /* device [B], taken into [0, Nk]; NULL: Nk.  Rows
+                              at kv_len and after may hold anything           */
+  const int32_t* q_start;  /* device [B], taken into [-2^30, 2^30]; NULL:
+                              kv_len[b] - Nq (the queries are the last tokens)*/
+  int64_t q_s[3], k_s[3], v_s[3], o_s[3];
+  int64_t do_s[3], dq_s[3], dk_s[3], dv_s[3];   /* backward                   */
+} vsa_window;
+
+/* O[p] = softmax_j(softmax_scale * q_p . k_j) V over the keys p sees, in the
+ * input type; lse: float32 [B, Hq, Nq], natural log of the denominator.
+ * Scores, softmax and sums in float32.  workspace as for the other calls (0
+ * bytes: may be NULL).  Any keys and queries that a mask leaves out
+ * altogether (rows at kv_len and after, queries that see nothing) may hold
+ * NaN or infinities; the others must be finite. */
+size_t vsa_window_attn_workspace_bytes(const vsa_window* w);
+int vsa_window_attn(const vsa_window* w, const void* q, const void* k, const void* v, float softmax_scale, void* o,
+                    float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its gradient: dO and what the forward call read and gave -> dQ, dK, dV in
+ * the input type.  Sums in float32, in a fixed order (the same bits each
+ * time).  Keys that no query sees get zeros. */
+size_t vsa_window_attn_bwd_workspace_bytes(const vsa_window* w);
+int vsa_window_attn_bwd(const vsa_window* w, const void* d_o, const void* q, const void* k, const void* v,
+                        const void* o, const float* lse, float softmax_scale, void* dq, void* dk, void* dv,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
 /* Reads (and with reset != 0 clears) the kernels' device error word on the
  * current device: 0 = no error; otherwise a VSA_DEVERR_* code.  Synchronizes
  * the device.  Returns a vsa_status for the read itself. */
