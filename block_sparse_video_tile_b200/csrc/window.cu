@@ -1,13 +1,16 @@
 // window.cu -- vsa_window_attn and its gradient: argument checks and launches
 // (declared in include/vsa.h).
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
 
 #include "vsa.h"
+#include "tma_encode.cuh"
 #include "vsa_host.h"
 #include "window_args.cuh"
+#include "window_fwd.cuh"
 #include "window_simple.cuh"
 
 namespace vsa {
@@ -49,6 +52,57 @@ static int win_bwd_strides(const vsa_window* w, WinArgs* a) {
   return VSA_OK;
 }
 
+// A strided head tensor as (d, N, H, B) with boxes of 64 channels x `rows`
+// rows of one head; reads past N give zeros, writes past N are dropped.
+static int encode_heads(CUtensorMap* m, const void* ptr, int B, int N, int H, int d, const long long s[3], int rows,
+                        bool f16) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (fn == nullptr) return VSA_ERR_CUDA;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(H),
+                        static_cast<cuuint64_t>(B)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(s[1]) * 2, static_cast<cuuint64_t>(s[2]) * 2,
+                           static_cast<cuuint64_t>(s[0]) * 2};
+  cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(rows), 1u, 1u};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  const CUresult r = fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                        const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? VSA_OK : VSA_ERR_CUDA;
+}
+
+// Splits of the blocks of a CTA of the forward kernel.
+static int win_fwd_splits(const WinArgs& a) {
+  return 1;
+}
+
+static size_t win_fwd_bytes(const WinArgs& a, int d, int splits) {
+  return splits == 1 ? 0 : static_cast<size_t>(splits) * a.B * a.Hq * a.Nq * (d + 1) * sizeof(float);
+}
+
+template <int D, bool F16>
+static int launch_fwd(const WinArgs& a, int splits, float* part, cudaStream_t st) {
+  CUtensorMap mq, mk, mv, mo;
+  int rc;
+  if ((rc = encode_heads(&mq, a.q, a.B, a.Nq, a.Hq, D, a.qs, 128, F16)) != VSA_OK ||
+      (rc = encode_heads(&mk, a.k, a.B, a.Nk, a.Hkv, D, a.ks, kWfKeys, F16)) != VSA_OK ||
+      (rc = encode_heads(&mv, a.v, a.B, a.Nk, a.Hkv, D, a.vs, kWfKeys, F16)) != VSA_OK ||
+      (rc = encode_heads(&mo, a.out, a.B, a.Nq, a.Hq, D, a.os, 128, F16)) != VSA_OK)
+    return rc;
+  if (cudaFuncSetAttribute(window_fwd_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           WfSmem<D>::kTotal) != cudaSuccess)
+    return VSA_ERR_CUDA;
+  const dim3 grid((a.Nq + kWfRows - 1) / kWfRows, a.Hq, a.B * splits);
+  window_fwd_kernel<D, F16><<<grid, kWfThreads, WfSmem<D>::kTotal, st>>>(mq, mk, mv, mo, a, splits, part);
+  if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
+  if (splits > 1) {
+    const long long rows = 1ll * a.B * a.Hq * a.Nq;
+    window_combine_kernel<D, F16><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(a, splits, part);
+    if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
+  }
+  return VSA_OK;
+}
+
 static size_t win_bwd_bytes(const vsa_window* w) {
   return (static_cast<size_t>(w->B) * w->Hq * w->Nq * sizeof(float) + 255) & ~static_cast<size_t>(255);
 }
@@ -62,7 +116,7 @@ extern "C" {
 size_t vsa_window_attn_workspace_bytes(const vsa_window* w) {
   WinArgs a;
   if (win_args(w, 1.f, &a) != VSA_OK) return 0;
-  return 0;
+  return win_fwd_bytes(a, w->d, win_fwd_splits(a));
 }
 
 int vsa_window_attn(const vsa_window* w, const void* q, const void* k, const void* v, float softmax_scale, void* o,
@@ -74,23 +128,21 @@ int vsa_window_attn(const vsa_window* w, const void* q, const void* k, const voi
   if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(o, 16) || !aligned_to(lse, 4) ||
       !aligned_to(workspace, 16))
     return VSA_ERR_ALIGNMENT;
+  const int splits = win_fwd_splits(a);
+  const size_t need = win_fwd_bytes(a, w->d, splits);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return VSA_ERR_WORKSPACE;
   if ((rc = check_arch()) != VSA_OK) return rc;
+  if ((a.err = device_error_ptr()) == nullptr) return VSA_ERR_CUDA;
   a.q = static_cast<const uint16_t*>(q);
   a.k = static_cast<const uint16_t*>(k);
   a.v = static_cast<const uint16_t*>(v);
   a.out = static_cast<uint16_t*>(o);
   a.lse = lse;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid((a.Nq + 7) / 8, a.Hq, a.B);
   const bool f16 = w->dtype == VSA_DTYPE_F16;
-  if (w->d == 128) {
-    if (f16) window_fwd_simple<128, true><<<grid, 256, 0, st>>>(a);
-    else window_fwd_simple<128, false><<<grid, 256, 0, st>>>(a);
-  } else {
-    if (f16) window_fwd_simple<64, true><<<grid, 256, 0, st>>>(a);
-    else window_fwd_simple<64, false><<<grid, 256, 0, st>>>(a);
-  }
-  return cudaGetLastError() == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
+  float* part = static_cast<float*>(workspace);
+  if (w->d == 128) return f16 ? launch_fwd<128, true>(a, splits, part, st) : launch_fwd<128, false>(a, splits, part, st);
+  return f16 ? launch_fwd<64, true>(a, splits, part, st) : launch_fwd<64, false>(a, splits, part, st);
 }
 
 size_t vsa_window_attn_bwd_workspace_bytes(const vsa_window* w) {

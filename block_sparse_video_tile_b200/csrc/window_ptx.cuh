@@ -1,0 +1,30 @@
+// window_ptx.cuh -- 4-D TMA copies of the strided head tensors and small
+// helpers shared by the window-attention kernels.
+#pragma once
+
+#include "vsa_ptx.cuh"
+
+namespace vsa {
+
+// Head tensors are seen by TMA as (d, N, H, B); a box is 64 channels of some
+// consecutive rows of one head (c0 in {0, 64}: 128-byte boundaries).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* desc, uint32_t bar, int c0, int n, int h, int b) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(desc)), "r"(bar), "r"(c0), "r"(n), "r"(h), "r"(b)
+      : "memory");
+}
+// Rows past N are not written.
+__device__ __forceinline__ void tma_store_4d(const void* desc, uint32_t src, int c0, int n, int h, int b) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group"
+      " [%0, {%2, %3, %4, %5}], [%1];" ::"l"(reinterpret_cast<uint64_t>(desc)),
+      "r"(src), "r"(c0), "r"(n), "r"(h), "r"(b)
+      : "memory");
+}
+
+// The lowest n bits (n may lie outside [0, 32]).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
+
+}  // namespace vsa

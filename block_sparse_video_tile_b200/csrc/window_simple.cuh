@@ -1,4 +1,4 @@
-// window_simple.cuh -- the window attention and its gradient, one warp per
+// window_simple.cuh -- the gradient of the window attention, one warp per
 // row: the formulas as they stand, lane c holding channels c, c + 32, ...
 #pragma once
 
@@ -32,36 +32,6 @@ __device__ __forceinline__ float dot(const float (&x)[D / 32], const float (&y)[
   float s = 0.f;
   for (int c = 0; c < D / 32; ++c) s = fmaf(x[c], y[c], s);
   return warp_sum(s);
-}
-
-// One warp per (query row, head, batch).
-template <int D, bool F16>
-__global__ void window_fwd_simple(const WinArgs a) {
-  const int lane = threadIdx.x % 32, i = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
-  const int h = blockIdx.y, b = blockIdx.z;
-  if (i >= a.Nq) return;
-  const int len = win_len(a, b);
-  const RowVis vis = row_vis(a, len, win_start(a, b, len) + i);
-  const uint16_t* kp = a.k + b * a.ks[0] + (h / a.group) * a.ks[2];
-  const uint16_t* vp = a.v + b * a.vs[0] + (h / a.group) * a.vs[2];
-  float q[D / 32], kv[D / 32], o[D / 32] = {};
-  load_row<D, F16>(a.q + b * a.qs[0] + i * a.qs[1] + h * a.qs[2], lane, q);
-  float m = -INFINITY, l = 0.f;
-  for (int j = vis.first > 0 ? 0 : vis.lo; j < vis.hi; ++j) {
-    if (j == vis.first && j < vis.lo) j = vis.lo;
-    if (j >= vis.hi) break;
-    load_row<D, F16>(kp + j * a.ks[1], lane, kv);
-    const float s = dot<D>(q, kv) * a.scale_log2;
-    const float mn = fmaxf(m, s), f = exp2f(m - mn), p = exp2f(s - mn);
-    load_row<D, F16>(vp + j * a.vs[1], lane, kv);
-    l = l * f + p;
-    for (int c = 0; c < D / 32; ++c) o[c] = o[c] * f + p * kv[c];
-    m = mn;
-  }
-  uint16_t* op = a.out + b * a.os[0] + i * a.os[1] + h * a.os[2];
-  for (int c = 0; c < D / 32; ++c) put<F16>(op + lane + 32 * c, l > 0.f ? o[c] / l : 0.f);
-  if (lane == 0)
-    a.lse[(static_cast<size_t>(b) * a.Hq + h) * a.Nq + i] = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
 }
 
 // One warp per (query row, head, batch): delta = dO . O and dQ.
