@@ -10,8 +10,8 @@
 #include "tma_encode.cuh"
 #include "vsa_host.h"
 #include "window_args.cuh"
+#include "window_bwd.cuh"
 #include "window_fwd.cuh"
-#include "window_simple.cuh"
 
 namespace vsa {
 
@@ -23,7 +23,7 @@ static int win_args(const vsa_window* w, float scale, WinArgs* a) {
   if (w->dtype != VSA_DTYPE_BF16 && w->dtype != VSA_DTYPE_F16) return VSA_ERR_UNSUPPORTED;
   if (!(scale > 0.f) || !std::isfinite(scale)) return VSA_ERR_INVALID_ARG;
   if (!aligned_to(w->kv_len, 4) || !aligned_to(w->q_start, 4)) return VSA_ERR_ALIGNMENT;
-  if (w->Nq > kWinMaxPos || w->Nk > kWinMaxPos || w->B > 65535 || w->Hq > 65535) return VSA_ERR_TOO_LARGE;
+  if (w->Nq > kWinMaxRows || w->Nk > kWinMaxRows || w->B > 65535 || w->Hq > 65535) return VSA_ERR_TOO_LARGE;
   a->B = w->B; a->Hq = w->Hq; a->Hkv = w->Hkv; a->group = w->Hq / w->Hkv;
   a->Nq = w->Nq; a->Nk = w->Nk;
   a->unit = w->unit;
@@ -107,6 +107,30 @@ static size_t win_bwd_bytes(const vsa_window* w) {
   return (static_cast<size_t>(w->B) * w->Hq * w->Nq * sizeof(float) + 255) & ~static_cast<size_t>(255);
 }
 
+// dQ (which also writes delta), then dK and dV.
+template <int D, bool F16>
+static int launch_bwd(const WinArgs& a, cudaStream_t st) {
+  CUtensorMap mq, mg, mk, mv, mdq, mdk, mdv;
+  int rc;
+  if ((rc = encode_heads(&mq, a.q, a.B, a.Nq, a.Hq, D, a.qs, kWbRows, F16)) != VSA_OK ||
+      (rc = encode_heads(&mg, a.d_o, a.B, a.Nq, a.Hq, D, a.dos, kWbRows, F16)) != VSA_OK ||
+      (rc = encode_heads(&mk, a.k, a.B, a.Nk, a.Hkv, D, a.ks, kWbRows, F16)) != VSA_OK ||
+      (rc = encode_heads(&mv, a.v, a.B, a.Nk, a.Hkv, D, a.vs, kWbRows, F16)) != VSA_OK ||
+      (rc = encode_heads(&mdq, a.dq, a.B, a.Nq, a.Hq, D, a.dqs, kWbRows, F16)) != VSA_OK ||
+      (rc = encode_heads(&mdk, a.dk, a.B, a.Nk, a.Hkv, D, a.dks, kWbRows, F16)) != VSA_OK ||
+      (rc = encode_heads(&mdv, a.dv, a.B, a.Nk, a.Hkv, D, a.dvs, kWbRows, F16)) != VSA_OK)
+    return rc;
+  constexpr int smem = WbSmem<D>::kTotal;
+  if (cudaFuncSetAttribute(window_dq_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      cudaFuncSetAttribute(window_dkv_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return VSA_ERR_CUDA;
+  window_dq_kernel<D, F16><<<dim3((a.Nq + kWbRows - 1) / kWbRows, a.Hq, a.B), kWbThreads, smem, st>>>(mq, mg, mk, mv, mdq, a);
+  if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
+  window_dkv_kernel<D, F16><<<dim3((a.Nk + kWbRows - 1) / kWbRows, a.Hkv, a.B), kWbThreads, smem, st>>>(mq, mg, mk, mv, mdk,
+                                                                                                      mdv, a);
+  return cudaGetLastError() == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
+}
+
 }  // namespace vsa
 
 using namespace vsa;
@@ -166,6 +190,7 @@ int vsa_window_attn_bwd(const vsa_window* w, const void* d_o, const void* q, con
   if (!aligned_to(lse, 4) || !aligned_to(workspace, 16)) return VSA_ERR_ALIGNMENT;
   if (workspace == nullptr || workspace_bytes < win_bwd_bytes(w)) return VSA_ERR_WORKSPACE;
   if ((rc = check_arch()) != VSA_OK) return rc;
+  if ((a.err = device_error_ptr()) == nullptr) return VSA_ERR_CUDA;
   a.q = static_cast<const uint16_t*>(q);
   a.k = static_cast<const uint16_t*>(k);
   a.v = static_cast<const uint16_t*>(v);
@@ -177,17 +202,9 @@ int vsa_window_attn_bwd(const vsa_window* w, const void* d_o, const void* q, con
   a.dv = static_cast<uint16_t*>(dv);
   a.delta = static_cast<float*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 gq((a.Nq + 7) / 8, a.Hq, a.B), gk((a.Nk + 7) / 8, a.Hkv, a.B);
   const bool f16 = w->dtype == VSA_DTYPE_F16;
-#define VSA_WIN_BWD(D, F)                          \
-  do {                                             \
-    window_dq_simple<D, F><<<gq, 256, 0, st>>>(a); \
-    window_dkv_simple<D, F><<<gk, 256, 0, st>>>(a); \
-  } while (0)
-  if (w->d == 128) { if (f16) VSA_WIN_BWD(128, true); else VSA_WIN_BWD(128, false); }
-  else { if (f16) VSA_WIN_BWD(64, true); else VSA_WIN_BWD(64, false); }
-#undef VSA_WIN_BWD
-  return cudaGetLastError() == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
+  if (w->d == 128) return f16 ? launch_bwd<128, true>(a, st) : launch_bwd<128, false>(a, st);
+  return f16 ? launch_bwd<64, true>(a, st) : launch_bwd<64, false>(a, st);
 }
 
 }  // extern "C"

@@ -27,7 +27,8 @@ struct WinArgs {
   unsigned int* err;
 };
 
-constexpr int kWinMaxPos = 1 << 30;
+constexpr int kWinMaxPos = 1 << 30;        // of q_start; start + row stays below 2^31
+constexpr int kWinMaxRows = (1 << 30) - 512;
 
 __device__ __forceinline__ int win_len(const WinArgs& a, int b) {
   return a.kv_len == nullptr ? a.Nk : min(max(__ldg(a.kv_len + b), 0), a.Nk);

@@ -1,0 +1,691 @@
+// window_bwd.cuh -- gradient of the window attention for sm_100a, from the
+// forward's O and LSE:
+//   P = exp(scale Q K^T - LSE),  dP = dO V^T,  delta = rowsum(dO * O),
+//   dS = P * (dP - delta),  dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO
+//
+// Two kernels, so that no sum is made by atomics and every result has the
+// same bits each time: window_dq_kernel walks the keys of 128 query rows
+// (three products a block: S, dP, dQ; it also writes delta), and
+// window_dkv_kernel walks the queries of 128 key rows, over all query heads
+// of the key/value head (four products: S^T, dP^T, dV, dK).  S and dP are
+// made twice: 7 products of 128 x 128 x d a block pair where 5 would do, in
+// exchange for no float32 dQ in memory (128 KB of atomic traffic a pair).
+//
+// Both are bound by the tensor pipe (1536 and 2048 clk a block at d = 128)
+// with the exponential unit (1024 clk) next.  The elementwise warps work on
+// the block in two halves of 64 columns (a warpgroup each, thread = row), and
+// write their 16-bit operand over the scores it came from, so P and dS never
+// leave TMEM.
+//
+// Rounding: P and dS are rounded to the 16-bit type as MMA operands; scores,
+// dP, delta and the accumulators are float32; results are rounded once.
+#pragma once
+
+#include <cuda.h>
+
+#include "window_args.cuh"
+#include "window_fwd.cuh"
+#include "window_ptx.cuh"
+
+namespace vsa {
+
+constexpr int kWbThreads = 384;
+constexpr int kWbRows = 128;             // rows a CTA, and rows of a block it walks
+
+template <int D>
+struct WbSmem {
+  static constexpr int kSlab = 128 * 128;
+  static constexpr int kSlabs = D / 64;
+  static constexpr int kBuf = kSlabs * kSlab;
+  static constexpr int kOwn0 = 0, kOwn1 = kBuf;        // the CTA's own two tiles
+  static constexpr int kASt = 3, kBSt = 2;             // stages of the walked tiles
+  static constexpr int kA = 2 * kBuf, kB = kA + kASt * kBuf;
+  static constexpr int kBar = kB + kBSt * kBuf;
+  static constexpr int kNumBars = 32;
+  static constexpr int kMisc = kBar + kNumBars * 8;
+  static constexpr int kXch = kMisc + 16;              // dq: float [128], delta between the warpgroups
+  // dkv: (-lse * log2 e, -delta) of the walked queries, float [2 stages][2][128], in place of the third A stage
+  static constexpr int kStats = kA + 2 * kBuf;
+  static constexpr int kTotal = kXch + 512 + 1024;     // 1024: alignment of the base
+};
+
+// Stages an O-shaped tile of this thread's row (128 columns of TMEM at t, D of
+// them) times f into `buf`, swizzled as the TMA boxes are.
+template <int D, bool F16>
+__device__ __forceinline__ void stage_row(uint32_t t, uint32_t buf, int r, float f, bool zero) {
+#pragma unroll
+  for (int q4 = 0; q4 < D / 32; ++q4) {
+    uint32_t ov[32];
+    if (!zero) {
+      tmem_ld32(t + 32u * q4, ov);
+      tmem_wait_ld();
+    }
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      pk[e] = zero ? 0u : pack_elem2<F16>(__uint_as_float(ov[2 * e]) * f, __uint_as_float(ov[2 * e + 1]) * f);
+    const uint32_t at = buf + r * 128u + (q4 >> 1) * WbSmem<D>::kSlab;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      st_shared_v4(at + static_cast<uint32_t>(((q4 & 1) * 4 + e) ^ (r & 7)) * 16u, pk[4 * e], pk[4 * e + 1],
+                   pk[4 * e + 2], pk[4 * e + 3]);
+  }
+}
+
+// Zeros row r of a 128-row tile.
+template <int D>
+__device__ __forceinline__ void zero_row(uint32_t buf, int r) {
+#pragma unroll
+  for (int sl = 0; sl < D / 64; ++sl)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) st_shared_v4(buf + sl * WbSmem<D>::kSlab + r * 128u + e * 16u, 0u, 0u, 0u, 0u);
+}
+
+// ------------------------------------------------------------------ dQ
+enum : int {
+  DQ_OWN = 0, DQ_S = 1 /* [2] */, DQ_DP = 3, DQ_DP_FREE = 4, DQ_DS = 5 /* [2] */, DQ_S_FREE = 7 /* [2] */, DQ_OUT = 9,
+  DQ_DRAIN = 10, DQ_K_FULL = 11, DQ_K_EMPTY = 14, DQ_V_FULL = 17, DQ_V_EMPTY = 19
+};
+
+// TMEM: two score buffers (dS of a warpgroup's 64 keys over the first 32
+// columns of its half), dP, dQ.  Scores run two blocks ahead.  Warps: 0-3 and
+// 4-7 elementwise (keys 0-63 and 64-127 of a block), 8 loads, 9 issues S, 10
+// dP, 11 dQ.
+template <int D, bool F16>
+__global__ void __launch_bounds__(kWbThreads, 1)
+    window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
+                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ CUtensorMap tmDQ, const __grid_constant__ WinArgs a) {
+  using L = WbSmem<D>;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char* sp = smem_raw + (base - raw);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sp + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + L::kMisc + 4);
+  auto bar = [&](int id) -> uint32_t { return base + L::kBar + 8u * static_cast<uint32_t>(id); };
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int h = blockIdx.y, b = blockIdx.z, hk = h / a.group;
+  const int i0 = (gridDim.x - 1 - blockIdx.x) * kWbRows;
+  const int len = win_len(a, b), start = win_start(a, b, len);
+  const WinBlocks wb = win_blocks(a, len, start, i0, min(i0 + kWbRows, a.Nq) - 1);
+  const int n = wb.count();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kNumBars; ++i) {
+      uint32_t cnt = 1;
+      if (i == DQ_DP_FREE || i == DQ_DS || i == DQ_DS + 1) cnt = 256;
+      if (i == DQ_DRAIN) cnt = 3;
+      mbar_init(bar(i), cnt);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 11) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tDP = tmem + 256, tDQ = tmem + 384;
+
+  if (warp == 8) {
+    // ====================================================== TMA producer
+    if (lane == 0 && n > 0) {
+      mbar_arrive_expect_tx(bar(DQ_OWN), 2 * L::kBuf);
+      for (int sl = 0; sl < L::kSlabs; ++sl) {
+        tma_load_4d(base + L::kOwn0 + sl * L::kSlab, &tmQ, bar(DQ_OWN), sl * 64, i0, h, b);
+        tma_load_4d(base + L::kOwn1 + sl * L::kSlab, &tmG, bar(DQ_OWN), sl * 64, i0, h, b);
+      }
+      int kd = 0, vd = 0;                              // loads issued
+      for (int j = 0; j < n; ++j) {
+        const int c0 = wb.block(j) * kWfKeys;
+        const int ks = j % L::kASt, vs = j % L::kBSt;
+        if (j >= L::kASt && !mbar_wait(bar(DQ_K_EMPTY + ks), (j / L::kASt - 1) & 1, abort_flag, a.err)) break;
+        kd = j + 1;
+        mbar_arrive_expect_tx(bar(DQ_K_FULL + ks), L::kBuf);
+        for (int sl = 0; sl < L::kSlabs; ++sl)
+          tma_load_4d(base + L::kA + ks * L::kBuf + sl * L::kSlab, &tmK, bar(DQ_K_FULL + ks), sl * 64, c0, hk, b);
+        if (j >= L::kBSt && !mbar_wait(bar(DQ_V_EMPTY + vs), (j / L::kBSt - 1) & 1, abort_flag, a.err)) break;
+        vd = j + 1;
+        mbar_arrive_expect_tx(bar(DQ_V_FULL + vs), L::kBuf);
+        for (int sl = 0; sl < L::kSlabs; ++sl)
+          tma_load_4d(base + L::kB + vs * L::kBuf + sl * L::kSlab, &tmV, bar(DQ_V_FULL + vs), sl * 64, c0, hk, b);
+      }
+      // let every issued copy land before the CTA can exit
+      for (int j = max(0, kd - L::kASt); j < kd; ++j)
+        mbar_wait(bar(DQ_K_FULL + j % L::kASt), (j / L::kASt) & 1, nullptr, a.err);
+      for (int j = max(0, vd - L::kBSt); j < vd; ++j)
+        mbar_wait(bar(DQ_V_FULL + j % L::kBSt), (j / L::kBSt) & 1, nullptr, a.err);
+      mbar_wait(bar(DQ_OWN), 0, nullptr, a.err);
+    }
+    __syncwarp();
+  } else if (warp >= 9) {
+    // ====================================================== MMA issuers
+    constexpr uint32_t idS = idesc_f16kind_f32(128, 128, false, F16);
+    constexpr uint32_t idQ = idesc_f16kind_f32(128, D, true, F16);
+    bool ok = n == 0 || __all_sync(0xffffffffu, mbar_wait(bar(DQ_OWN), 0, abort_flag, a.err));
+    for (int j = 0; j < n && ok; ++j) {
+      const int ks = j % L::kASt, vs = j % L::kBSt, sb = j & 1;
+      const uint32_t kb = base + L::kA + ks * L::kBuf, vb = base + L::kB + vs * L::kBuf;
+      if (warp == 9) {                                 // S(j) once K(j) is in and dQ(j-2) has read dS(j-2)
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(DQ_K_FULL + ks), (j / L::kASt) & 1, abort_flag, a.err) &&
+                                         (j < 2 || mbar_wait(bar(DQ_S_FREE + sb), ((j >> 1) - 1) & 1, abort_flag, a.err)));
+      } else if (warp == 10) {                         // dP(j) once V(j) is in and dP(j-1) has been read
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(DQ_V_FULL + vs), (j / L::kBSt) & 1, abort_flag, a.err) &&
+                                         (j < 1 || mbar_wait(bar(DQ_DP_FREE), (j - 1) & 1, abort_flag, a.err)));
+      } else {                                         // dQ += dS(j) K(j)
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(DQ_K_FULL + ks), (j / L::kASt) & 1, abort_flag, a.err) &&
+                                         mbar_wait(bar(DQ_DS + sb), (j >> 1) & 1, abort_flag, a.err));
+      }
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one_sync()) {
+        if (warp == 9) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const int off = (kk / 4) * L::kSlab + (kk % 4) * 32;
+            mma_ss(tmem + 128u * sb, smem_desc_sw128(base + L::kOwn0 + off, 16, 1024), smem_desc_sw128(kb + off, 16, 1024),
+                   idS, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(bar(DQ_S + sb));
+        } else if (warp == 10) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const int off = (kk / 4) * L::kSlab + (kk % 4) * 32;
+            mma_ss(tDP, smem_desc_sw128(base + L::kOwn1 + off, 16, 1024), smem_desc_sw128(vb + off, 16, 1024), idS,
+                   kk > 0 ? 1u : 0u);
+          }
+          mma_commit(bar(DQ_DP));
+          mma_commit(bar(DQ_V_EMPTY + vs));
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)               // 16 keys a step: 8 columns of a warpgroup's 32
+            mma_ts(tDQ, tmem + 128u * sb + 64u * (kk / 4) + 8u * (kk % 4), smem_desc_sw128(kb + kk * 2048, L::kSlab, 1024),
+                   idQ, (j > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(bar(DQ_K_EMPTY + ks));
+          mma_commit(bar(DQ_S_FREE + sb));
+          if (j == n - 1) mma_commit(bar(DQ_OUT));
+        }
+      }
+      __syncwarp();
+    }
+    if (elect_one_sync()) mma_commit(bar(DQ_DRAIN));
+    __syncwarp();
+    mbar_wait(bar(DQ_DRAIN), 0, nullptr, a.err);
+  } else {
+    // ====================================================== elementwise
+    const int w = warp / 4, r = threadIdx.x % 128;
+    const int i = i0 + r;
+    const uint32_t lane_base = static_cast<uint32_t>((warp % 4) * 32) << 16;
+    RowVis vis{0, 0, 0};
+    float lse2 = 0.f, delta = 0.f;
+    const size_t row = (static_cast<size_t>(b) * a.Hq + h) * a.Nq + i;
+    if (i < a.Nq) {
+      vis = row_vis(a, len, start + i);
+      const float ls = a.lse[row];
+      lse2 = ls == -INFINITY ? 0.f : ls * 1.4426950408889634f;
+      // delta: this warpgroup's half of the channels, then both halves
+      const uint4* op = reinterpret_cast<const uint4*>(a.o + b * a.os[0] + i * a.os[1] + h * a.os[2]) + w * (D / 16);
+      const uint4* gp = reinterpret_cast<const uint4*>(a.d_o + b * a.dos[0] + i * a.dos[1] + h * a.dos[2]) + w * (D / 16);
+#pragma unroll
+      for (int e = 0; e < D / 16; ++e) {
+        const uint4 x = __ldg(op + e), g = __ldg(gp + e);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, gs[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float2 xf = unpack_elem2<F16>(xs[u]), gf = unpack_elem2<F16>(gs[u]);
+          delta = fmaf(xf.x, gf.x, fmaf(xf.y, gf.y, delta));
+        }
+      }
+    }
+    float* xch = reinterpret_cast<float*>(sp + L::kXch);
+    if (w == 1) xch[r] = delta;
+    named_bar_sync(1, 256);
+    const float other = xch[r];
+    if (w == 0) delta += other;
+    named_bar_sync(1, 256);
+    if (w == 0) xch[r] = delta;
+    named_bar_sync(1, 256);
+    delta = xch[r];
+    if (w == 0 && i < a.Nq) a.delta[row] = delta;
+
+    bool ok = true;
+    const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2), nl2 = f2_pack(-lse2, -lse2), nd2 = f2_pack(-delta, -delta);
+    for (int j = 0; j < n; ++j) {
+      const int c0 = wb.block(j) * kWfKeys, sb = j & 1;
+      const uint32_t tS = tmem + lane_base + 128u * sb + 64u * w, tP = tDP + lane_base + 64u * w;
+      const bool row_full = i >= a.Nq || c0 + kWfKeys <= vis.first || (c0 >= vis.lo && c0 + kWfKeys <= vis.hi);
+      const bool masked = __any_sync(0xffffffffu, !row_full);
+      // Keys that no row of the CTA sees may hold anything: zero their K rows
+      // (0 * NaN would reach dQ).
+      if ((c0 + kWfKeys > wb.hi || c0 < wb.lo) && c0 + kWfKeys > wb.first) {
+        const int ks = j % L::kASt, key = c0 + r;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(DQ_K_FULL + ks), (j / L::kASt) & 1, abort_flag, a.err))) {
+          ok = false;
+          break;
+        }
+        if (w == 0 && key >= wb.first && (key < wb.lo || key >= wb.hi)) zero_row<D>(base + L::kA + ks * L::kBuf, r);
+        fence_proxy_async_smem();
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(DQ_S + sb), (j >> 1) & 1, abort_flag, a.err))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t x[64], g[64];
+      tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+      tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        float z0, z1;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sc2, nl2), z0, z1);
+        x[2 * e] = __float_as_uint(ex2_approx(z0));
+        x[2 * e + 1] = __float_as_uint(ex2_approx(z1));
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(DQ_DP), j & 1, abort_flag, a.err))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      tmem_ld32(tP, *reinterpret_cast<uint32_t(*)[32]>(&g[0]));
+      tmem_ld32(tP + 32, *reinterpret_cast<uint32_t(*)[32]>(&g[32]));
+      tmem_wait_ld();
+      tc_fence_before();
+      mbar_arrive(bar(DQ_DP_FREE));
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        float d0, d1;
+        f2_unpack(f2_add(f2_pack(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1])), nd2), d0, d1);
+        x[2 * e] = __float_as_uint(__uint_as_float(x[2 * e]) * d0);
+        x[2 * e + 1] = __float_as_uint(__uint_as_float(x[2 * e + 1]) * d1);
+      }
+      if (masked) {
+        uint32_t mw[4];
+        vis_words(vis, c0, mw);
+        const uint32_t m0 = w == 0 ? mw[0] : mw[2], m1 = w == 0 ? mw[1] : mw[3];
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (!(((e < 32 ? m0 : m1) >> (e & 31)) & 1u)) x[e] = 0u;
+      }
+#pragma unroll
+      for (int e = 0; e < 32; ++e) x[e] = pack_elem2<F16>(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+      tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar(DQ_DS + sb));
+    }
+    // ---- epilogue: warpgroup 0 writes dQ through Q's buffer
+    if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(DQ_OUT), 0, abort_flag, a.err));
+    tc_fence_after();
+    if (w == 0) {
+      if (n > 0) {
+        if (ok) stage_row<D, F16>(tDQ + lane_base, base + L::kOwn0, r, a.scale, false);
+        fence_proxy_async_smem();
+        named_bar_sync(2, 128);
+        if (ok && r == 0) {
+          for (int sl = 0; sl < L::kSlabs; ++sl)
+            tma_store_4d(&tmDQ, base + L::kOwn0 + sl * L::kSlab, sl * 64, i0, h, b);
+          bulk_commit_group();
+          bulk_wait_group_read0();
+        }
+      } else if (i < a.Nq) {
+        uint4* o = reinterpret_cast<uint4*>(a.dq + b * a.dqs[0] + i * a.dqs[1] + h * a.dqs[2]);
+#pragma unroll
+        for (int e = 0; e < D / 8; ++e) o[e] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 11) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ dK, dV
+enum : int {
+  DK_OWN = 0, DK_S = 1, DK_P = 2 /* [half] */, DK_DP = 4, DK_DS = 5, DK_OUT = 6 /* [2] */, DK_DRAIN = 8,
+  DK_Q_FULL = 9 /* [2] */, DK_Q_EMPTY = 11, DK_G_FULL = 13, DK_G_EMPTY = 15, DK_ST_FULL = 17, DK_ST_EMPTY = 19
+};
+
+// The CTA's 128 keys are the rows, the queries of a block the columns.  TMEM:
+// S^T, dP^T, dV, dK; P^T and dS^T of a warpgroup's 64 queries over the first
+// 32 columns of its half.  One warp issues dV(j) and right behind it S(j+1),
+// another dK(j) and dP(j+1): the next scores are made while the elementwise
+// warps finish dS.  P^T is released in two parts, so dV starts before the
+// exponentials end.  Warps: 0-7 elementwise, 8 loads, 9 fetches LSE and delta
+// of the walked queries, 10 issues S and dV, 11 dP and dK.
+template <int D, bool F16>
+__global__ void __launch_bounds__(kWbThreads, 1)
+    window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
+                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ CUtensorMap tmDK, const __grid_constant__ CUtensorMap tmDV,
+                      const __grid_constant__ WinArgs a) {
+  using L = WbSmem<D>;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char* sp = smem_raw + (base - raw);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sp + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + L::kMisc + 4);
+  float* stats = reinterpret_cast<float*>(sp + L::kStats);
+  auto bar = [&](int id) -> uint32_t { return base + L::kBar + 8u * static_cast<uint32_t>(id); };
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int hk = blockIdx.y, b = blockIdx.z;
+  const int c0 = blockIdx.x * kWbRows;                 // first keys first: they may be seen by every query
+  const int len = win_len(a, b), start = win_start(a, b, len);
+  // queries that see some key of [c0, c1): one range of rows, [qlo, qhi)
+  int qb0 = 0, nq = 0;
+  if (c0 < len) {
+    const int c1 = min(c0 + kWbRows, len);
+    const long long p0 = static_cast<long long>(c0 / a.unit) * a.unit;
+    const long long p1 = c0 < a.sink_tok ? (1ll << 40) : ((c1 - 1) / a.unit + static_cast<long long>(a.window)) * a.unit;
+    const long long qlo = max(p0 - start, 0ll), qhi = min(p1 - start, static_cast<long long>(a.Nq));
+    if (qhi > qlo) {
+      qb0 = static_cast<int>(qlo / kWbRows);
+      nq = static_cast<int>((qhi + kWbRows - 1) / kWbRows) - qb0;
+    }
+  }
+  const int n = nq * a.group;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kNumBars; ++i) {
+      uint32_t cnt = 1;
+      if (i == DK_P || i == DK_P + 1 || i == DK_DS || i == DK_ST_EMPTY || i == DK_ST_EMPTY + 1) cnt = 256;
+      if (i == DK_DRAIN || (i >= DK_Q_EMPTY && i < DK_Q_EMPTY + 2) || (i >= DK_G_EMPTY && i < DK_G_EMPTY + 2)) cnt = 2;
+      if (i == DK_ST_FULL || i == DK_ST_FULL + 1) cnt = 32;
+      mbar_init(bar(i), cnt);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 11) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tS = tmem, tDP = tmem + 128, tDV = tmem + 256, tDK = tmem + 384;
+  // walked block j: query head hk * group + j / nq, rows from (qb0 + j % nq) * 128
+
+  if (warp == 8) {
+    // ====================================================== TMA producer
+    if (lane == 0 && n > 0) {
+      mbar_arrive_expect_tx(bar(DK_OWN), 2 * L::kBuf);
+      for (int sl = 0; sl < L::kSlabs; ++sl) {
+        tma_load_4d(base + L::kOwn0 + sl * L::kSlab, &tmK, bar(DK_OWN), sl * 64, c0, hk, b);
+        tma_load_4d(base + L::kOwn1 + sl * L::kSlab, &tmV, bar(DK_OWN), sl * 64, c0, hk, b);
+      }
+      int qd = 0, gd = 0, h = hk * a.group, qi = 0;
+      for (int j = 0; j < n; ++j) {
+        const int st = j & 1, i0 = (qb0 + qi) * kWbRows;
+        if (j >= 2 && !mbar_wait(bar(DK_Q_EMPTY + st), ((j >> 1) - 1) & 1, abort_flag, a.err)) break;
+        qd = j + 1;
+        mbar_arrive_expect_tx(bar(DK_Q_FULL + st), L::kBuf);
+        for (int sl = 0; sl < L::kSlabs; ++sl)
+          tma_load_4d(base + L::kA + st * L::kBuf + sl * L::kSlab, &tmQ, bar(DK_Q_FULL + st), sl * 64, i0, h, b);
+        if (j >= 2 && !mbar_wait(bar(DK_G_EMPTY + st), ((j >> 1) - 1) & 1, abort_flag, a.err)) break;
+        gd = j + 1;
+        mbar_arrive_expect_tx(bar(DK_G_FULL + st), L::kBuf);
+        for (int sl = 0; sl < L::kSlabs; ++sl)
+          tma_load_4d(base + L::kB + st * L::kBuf + sl * L::kSlab, &tmG, bar(DK_G_FULL + st), sl * 64, i0, h, b);
+        if (++qi == nq) { qi = 0; ++h; }
+      }
+      for (int j = max(0, qd - 2); j < qd; ++j) mbar_wait(bar(DK_Q_FULL + (j & 1)), (j >> 1) & 1, nullptr, a.err);
+      for (int j = max(0, gd - 2); j < gd; ++j) mbar_wait(bar(DK_G_FULL + (j & 1)), (j >> 1) & 1, nullptr, a.err);
+      mbar_wait(bar(DK_OWN), 0, nullptr, a.err);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ====================================================== LSE and delta
+    int h = hk * a.group, qi = 0;
+    for (int j = 0; j < n; ++j) {
+      const int st = j & 1, i0 = (qb0 + qi) * kWbRows;
+      const size_t row0 = (static_cast<size_t>(b) * a.Hq + h) * a.Nq;
+      float ls[4], de[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = i0 + 32 * e + lane;
+        ls[e] = i < a.Nq ? a.lse[row0 + i] : 0.f;
+        de[e] = i < a.Nq ? a.delta[row0 + i] : 0.f;
+      }
+      if (j >= 2 &&
+          !__all_sync(0xffffffffu, mbar_wait(bar(DK_ST_EMPTY + st), ((j >> 1) - 1) & 1, abort_flag, a.err)))
+        break;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        stats[st * 256 + 32 * e + lane] = ls[e] == -INFINITY ? 0.f : -ls[e] * 1.4426950408889634f;
+        stats[st * 256 + 128 + 32 * e + lane] = -de[e];
+      }
+      mbar_arrive(bar(DK_ST_FULL + st));
+      if (++qi == nq) { qi = 0; ++h; }
+    }
+  } else if (warp >= 10) {
+    // ====================================================== MMA issuers
+    constexpr uint32_t idS = idesc_f16kind_f32(128, 128, false, F16);
+    constexpr uint32_t idO = idesc_f16kind_f32(128, D, true, F16);
+    const bool first = warp == 10;                     // S, dV; else dP, dK
+    bool ok = n == 0 || __all_sync(0xffffffffu, mbar_wait(bar(DK_OWN), 0, abort_flag, a.err));
+    // S(j) = K Q(j)^T, or dP(j) = V dO(j)^T
+    auto make = [&](int j) {
+      const int st = j & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar((first ? DK_Q_FULL : DK_G_FULL) + st), (j >> 1) & 1, abort_flag, a.err));
+      if (!ok) return;
+      tc_fence_after();
+      if (elect_one_sync()) {
+        const uint32_t own = base + (first ? L::kOwn0 : L::kOwn1);
+        const uint32_t in = base + (first ? L::kA : L::kB) + st * L::kBuf;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const int off = (kk / 4) * L::kSlab + (kk % 4) * 32;
+          mma_ss(first ? tS : tDP, smem_desc_sw128(own + off, 16, 1024), smem_desc_sw128(in + off, 16, 1024), idS,
+                 kk > 0 ? 1u : 0u);
+        }
+        mma_commit(bar(first ? DK_S : DK_DP));
+        mma_commit(bar((first ? DK_Q_EMPTY : DK_G_EMPTY) + st));
+      }
+      __syncwarp();
+    };
+    if (ok && n > 0) make(0);
+    for (int j = 0; j < n && ok; ++j) {
+      const int st = j & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar((first ? DK_G_FULL : DK_Q_FULL) + st), (j >> 1) & 1, abort_flag, a.err));
+      if (!ok) break;
+      if (first) {
+        const uint32_t gb = base + L::kB + st * L::kBuf;
+#pragma unroll
+        for (int hf = 0; hf < 2 && ok; ++hf) {
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(DK_P + hf), j & 1, abort_flag, a.err));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one_sync()) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int kk = 4 * (e >> 1) + 2 * hf + (e & 1);      // queries 16 kk .. 16 kk + 15
+              mma_ts(tDV, tS + 64u * (kk / 4) + 8u * (kk % 4), smem_desc_sw128(gb + kk * 2048, L::kSlab, 1024), idO,
+                     (j > 0 || hf > 0 || e > 0) ? 1u : 0u);
+            }
+            if (hf == 1) {
+              mma_commit(bar(DK_G_EMPTY + st));
+              if (j == n - 1) mma_commit(bar(DK_OUT));
+            }
+          }
+          __syncwarp();
+        }
+      } else {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(DK_DS), j & 1, abort_flag, a.err));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one_sync()) {
+          const uint32_t qb = base + L::kA + st * L::kBuf;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(tDK, tDP + 64u * (kk / 4) + 8u * (kk % 4), smem_desc_sw128(qb + kk * 2048, L::kSlab, 1024), idO,
+                   (j > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(bar(DK_Q_EMPTY + st));
+          if (j == n - 1) mma_commit(bar(DK_OUT + 1));
+        }
+        __syncwarp();
+      }
+      if (ok && j + 1 < n) make(j + 1);
+    }
+    if (elect_one_sync()) mma_commit(bar(DK_DRAIN));
+    __syncwarp();
+    mbar_wait(bar(DK_DRAIN), 0, nullptr, a.err);
+  } else {
+    // ====================================================== elementwise
+    const int w = warp / 4, r = threadIdx.x % 128;
+    const int key = c0 + r;
+    const uint32_t lane_base = static_cast<uint32_t>((warp % 4) * 32) << 16;
+    const uint32_t tSw = tS + lane_base + 64u * w, tPw = tDP + lane_base + 64u * w;
+    // the query rows that see this key: [qlo, qhi)
+    int qlo = 0, qhi = 0;
+    if (key < len) {
+      const int u = key / a.unit;
+      const long long p0 = static_cast<long long>(u) * a.unit;
+      const long long p1 = key < a.sink_tok ? (1ll << 40) : (static_cast<long long>(u) + a.window) * a.unit;
+      qlo = static_cast<int>(min(max(p0 - start, 0ll), static_cast<long long>(a.Nq)));
+      qhi = static_cast<int>(min(max(p1 - start, 0ll), static_cast<long long>(a.Nq)));
+    }
+    bool ok = true;
+    const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2);
+    int qi = 0;
+    for (int j = 0; j < n; ++j) {
+      const int st = j & 1, i0 = (qb0 + qi) * kWbRows;
+      if (++qi == nq) qi = 0;
+      const bool masked = __any_sync(0xffffffffu, qlo > i0 || qhi < i0 + kWbRows);
+      // Queries that see nothing may hold anything: zero their Q and dO rows.
+      // They are the rows before position 0, and those whose window lies
+      // behind the last key.
+      const int il = min(i0 + kWbRows, a.Nq) - 1;
+      if (start + i0 < 0 || (masked && row_vis(a, len, start + il).hi == row_vis(a, len, start + il).lo &&
+                             row_vis(a, len, start + il).first == 0)) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(DK_Q_FULL + st), (j >> 1) & 1, abort_flag, a.err) &&
+                                         mbar_wait(bar(DK_G_FULL + st), (j >> 1) & 1, abort_flag, a.err))) {
+          ok = false;
+          break;
+        }
+        const RowVis v = row_vis(a, len, start + i0 + r);
+        if (v.hi == v.lo && v.first == 0 && i0 + r < a.Nq)
+          zero_row<D>(base + (w == 0 ? L::kA : L::kB) + st * L::kBuf, r);
+        fence_proxy_async_smem();
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(DK_ST_FULL + st), (j >> 1) & 1, abort_flag, a.err) &&
+                                       mbar_wait(bar(DK_S), j & 1, abort_flag, a.err))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const float4* nl = reinterpret_cast<const float4*>(stats + st * 256 + 64 * w);
+      const float4* nd = reinterpret_cast<const float4*>(stats + st * 256 + 128 + 64 * w);
+      uint32_t x[64];
+      tmem_ld32(tSw, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+      tmem_ld32(tSw + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+      tmem_wait_ld();
+      uint32_t m0 = ~0u, m1 = ~0u;
+      if (masked) {
+        const int q0 = i0 + 64 * w;
+        m0 = low_bits(qhi - q0) & ~low_bits(qlo - q0);
+        m1 = low_bits(qhi - q0 - 32) & ~low_bits(qlo - q0 - 32);
+      }
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 8 * hf; e < 8 * hf + 8; ++e) {
+          const float4 l4 = nl[e];
+          float z0, z1, z2, z3;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])), sc2, f2_pack(l4.x, l4.y)), z0, z1);
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])), sc2, f2_pack(l4.z, l4.w)), z2, z3);
+          x[4 * e] = __float_as_uint(ex2_approx(z0));
+          x[4 * e + 1] = __float_as_uint(ex2_approx(z1));
+          x[4 * e + 2] = __float_as_uint(ex2_approx(z2));
+          x[4 * e + 3] = __float_as_uint(ex2_approx(z3));
+        }
+        if (masked) {
+#pragma unroll
+          for (int e = 32 * hf; e < 32 * hf + 32; ++e)
+            if (!(((hf == 0 ? m0 : m1) >> (e & 31)) & 1u)) x[e] = 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          pk[e] = pack_elem2<F16>(__uint_as_float(x[32 * hf + 2 * e]), __uint_as_float(x[32 * hf + 2 * e + 1]));
+        tmem_st16(tSw + 16u * hf, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(DK_P + hf));
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(DK_DP), j & 1, abort_flag, a.err))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t g[64], pk[32];
+      tmem_ld32(tPw, *reinterpret_cast<uint32_t(*)[32]>(&g[0]));
+      tmem_ld32(tPw + 32, *reinterpret_cast<uint32_t(*)[32]>(&g[32]));
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float4 d4 = nd[e];
+        float d0, d1, d2, d3;
+        f2_unpack(f2_add(f2_pack(__uint_as_float(g[4 * e]), __uint_as_float(g[4 * e + 1])), f2_pack(d4.x, d4.y)), d0, d1);
+        f2_unpack(f2_add(f2_pack(__uint_as_float(g[4 * e + 2]), __uint_as_float(g[4 * e + 3])), f2_pack(d4.z, d4.w)), d2, d3);
+        if (masked) {                                  // (P is 0 there, but dP may not be finite)
+          const uint32_t mm = (e < 8 ? m0 : m1) >> ((4 * e) & 31);
+          if (!(mm & 1u)) d0 = 0.f;
+          if (!(mm & 2u)) d1 = 0.f;
+          if (!(mm & 4u)) d2 = 0.f;
+          if (!(mm & 8u)) d3 = 0.f;
+        }
+        pk[2 * e] = pack_elem2<F16>(__uint_as_float(x[4 * e]) * d0, __uint_as_float(x[4 * e + 1]) * d1);
+        pk[2 * e + 1] = pack_elem2<F16>(__uint_as_float(x[4 * e + 2]) * d2, __uint_as_float(x[4 * e + 3]) * d3);
+      }
+      tmem_st32(tPw, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar(DK_DS));
+      mbar_arrive(bar(DK_ST_EMPTY + st));
+    }
+    // ---- epilogue: warpgroup 0 writes dV through V's buffer, 1 dK through K's
+    if (n > 0) {
+      if (ok)
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(DK_OUT), 0, abort_flag, a.err) &&
+                                         mbar_wait(bar(DK_OUT + 1), 0, abort_flag, a.err));
+      tc_fence_after();
+      const uint32_t buf = base + (w == 0 ? L::kOwn1 : L::kOwn0);
+      if (ok) stage_row<D, F16>((w == 0 ? tDV : tDK) + lane_base, buf, r, w == 0 ? 1.f : a.scale, false);
+      fence_proxy_async_smem();
+      named_bar_sync(1 + w, 128);
+      if (ok && r == 0) {
+        for (int sl = 0; sl < L::kSlabs; ++sl)
+          tma_store_4d(w == 0 ? &tmDV : &tmDK, buf + sl * L::kSlab, sl * 64, c0, hk, b);
+        bulk_commit_group();
+        bulk_wait_group_read0();
+      }
+    } else if (key < a.Nk) {                           // keys that no query sees
+      uint4* o = reinterpret_cast<uint4*>(w == 0 ? a.dv + b * a.dvs[0] + key * a.dvs[1] + hk * a.dvs[2]
+                                                 : a.dk + b * a.dks[0] + key * a.dks[1] + hk * a.dks[2]);
+#pragma unroll
+      for (int e = 0; e < D / 8; ++e) o[e] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 11) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace vsa

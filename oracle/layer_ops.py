@@ -111,8 +111,10 @@ def window_fwd(q, k, v, sees, scale, u):
 
 
 def window_bwd(do, q, k, v, sees, scale, u):
-    """(dq, dk, dv) and bounds on what they may differ by: P and dS are rounded once to the 16-bit type, O (inside
+    """(dq, dk, dv) and bounds on what they may differ by: P and dS are rounded once to the 16-bit type (fp16, half a
+    step u = 2^-11, has no steps finer than 2^-24, so values below its normal range are off by up to 2^-25), O (inside
     delta) is the forward's."""
+    low = 2.0 ** -25 if u == 2.0 ** -11 else 0.0
     B, Hq, Nq, d = q.shape
     Hkv = k.shape[1]
     g = Hq // Hkv
@@ -130,11 +132,11 @@ def window_bwd(do, q, k, v, sees, scale, u):
             dS = P * (dP - delta) * scale
             rel = (2 * bl[b, h])[:, None]                          # of P, from its score and its LSE
             E = scale * P * ((u + rel) * np.abs(dP - delta) + SCORE * (np.abs(G) @ np.abs(V).T)
-                             + (np.abs(G) * bo[b, h]).sum(-1, keepdims=True))
+                             + (np.abs(G) * bo[b, h]).sum(-1, keepdims=True)) + scale * low * see
             out[0][b, h] = dS @ K
             out[1][b, h // g] += dS.T @ Q
             out[2][b, h // g] += P.T @ G
             tol[0][b, h] = E @ np.abs(K)
             tol[1][b, h // g] += E.T @ np.abs(Q)
-            tol[2][b, h // g] += (P * (u + rel)).T @ np.abs(G)
+            tol[2][b, h // g] += (P * (u + rel) + low * see).T @ np.abs(G)
     return out, [t + u * 1.01 * np.abs(o) + 2.0 ** -23 for t, o in zip(tol, out)]
