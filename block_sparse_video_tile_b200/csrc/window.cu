@@ -12,6 +12,7 @@
 #include "window_args.cuh"
 #include "window_bwd.cuh"
 #include "window_fwd.cuh"
+#include "window_step.cuh"
 
 namespace vsa {
 
@@ -71,13 +72,54 @@ static int encode_heads(CUtensorMap* m, const void* ptr, int B, int N, int H, in
   return r == CUDA_SUCCESS ? VSA_OK : VSA_ERR_CUDA;
 }
 
-// Splits of the blocks of a CTA of the forward kernel.
-static int win_fwd_splits(const WinArgs& a) {
-  return 1;
+// How a forward call is run: few rows a key/value head (at most kWsMaxRows)
+// take the step kernel, others the tcgen05 kernel; either splits its keys
+// when its CTAs are too few, as far as the most keys that a row can see allow
+// (the lengths are on the device).
+constexpr int kWsMaxRows = 64;
+
+struct WinPlan {
+  bool step;
+  int splits;
+};
+
+static WinPlan win_plan(const WinArgs& a) {
+  WinPlan p;
+  const long long rows = 1ll * a.Nq * a.group;
+  p.step = rows <= kWsMaxRows && a.Hkv * ((rows + kWsRows - 1) / kWsRows) <= 65535;      // (grid.y)
+  const long long keys = std::min<long long>(
+      a.Nk, std::min(a.sink_tok, 1ll << 32) + std::min((a.window + 1ll) * a.unit, 1ll << 32) + a.Nq);
+  if (p.step) {
+    const long long ctas = 1ll * a.B * a.Hkv * ((rows + kWsRows - 1) / kWsRows);
+    const long long most = std::max(1ll, keys / (kWsKeys * kWsWarps * 2));   // two tiles a warp at least
+    p.splits = static_cast<int>(std::max(1ll, std::min({(148 * 8 + ctas - 1) / ctas, most, 256ll})));
+  } else {
+    p.splits = 1;
+  }
+  return p;
 }
 
 static size_t win_fwd_bytes(const WinArgs& a, int d, int splits) {
   return splits == 1 ? 0 : static_cast<size_t>(splits) * a.B * a.Hq * a.Nq * (d + 1) * sizeof(float);
+}
+
+template <int D, bool F16>
+static int launch_combine(const WinArgs& a, int splits, const float* part, cudaStream_t st) {
+  if (splits == 1) return VSA_OK;
+  const long long rows = 1ll * a.B * a.Hq * a.Nq;
+  window_combine_kernel<D, F16><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(a, splits, part);
+  return cudaGetLastError() == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
+}
+
+template <int D, bool F16>
+static int launch_step(const WinArgs& a, int splits, float* part, cudaStream_t st) {
+  constexpr int smem = WsSmem<D>::kTotal;
+  if (cudaFuncSetAttribute(window_step_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return VSA_ERR_CUDA;
+  const int tiles = (a.Nq * a.group + kWsRows - 1) / kWsRows;
+  window_step_kernel<D, F16><<<dim3(splits, a.Hkv * tiles, a.B), kWsThreads, smem, st>>>(a, splits, part);
+  if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
+  return launch_combine<D, F16>(a, splits, part, st);
 }
 
 template <int D, bool F16>
@@ -95,12 +137,12 @@ static int launch_fwd(const WinArgs& a, int splits, float* part, cudaStream_t st
   const dim3 grid((a.Nq + kWfRows - 1) / kWfRows, a.Hq, a.B * splits);
   window_fwd_kernel<D, F16><<<grid, kWfThreads, WfSmem<D>::kTotal, st>>>(mq, mk, mv, mo, a, splits, part);
   if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
-  if (splits > 1) {
-    const long long rows = 1ll * a.B * a.Hq * a.Nq;
-    window_combine_kernel<D, F16><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(a, splits, part);
-    if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
-  }
-  return VSA_OK;
+  return launch_combine<D, F16>(a, splits, part, st);
+}
+
+template <int D, bool F16>
+static int launch_any(const WinArgs& a, const WinPlan& p, float* part, cudaStream_t st) {
+  return p.step ? launch_step<D, F16>(a, p.splits, part, st) : launch_fwd<D, F16>(a, p.splits, part, st);
 }
 
 static size_t win_bwd_bytes(const vsa_window* w) {
@@ -140,7 +182,7 @@ extern "C" {
 size_t vsa_window_attn_workspace_bytes(const vsa_window* w) {
   WinArgs a;
   if (win_args(w, 1.f, &a) != VSA_OK) return 0;
-  return win_fwd_bytes(a, w->d, win_fwd_splits(a));
+  return win_fwd_bytes(a, w->d, win_plan(a).splits);
 }
 
 int vsa_window_attn(const vsa_window* w, const void* q, const void* k, const void* v, float softmax_scale, void* o,
@@ -152,8 +194,8 @@ int vsa_window_attn(const vsa_window* w, const void* q, const void* k, const voi
   if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(o, 16) || !aligned_to(lse, 4) ||
       !aligned_to(workspace, 16))
     return VSA_ERR_ALIGNMENT;
-  const int splits = win_fwd_splits(a);
-  const size_t need = win_fwd_bytes(a, w->d, splits);
+  const WinPlan plan = win_plan(a);
+  const size_t need = win_fwd_bytes(a, w->d, plan.splits);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return VSA_ERR_WORKSPACE;
   if ((rc = check_arch()) != VSA_OK) return rc;
   if ((a.err = device_error_ptr()) == nullptr) return VSA_ERR_CUDA;
@@ -165,8 +207,8 @@ int vsa_window_attn(const vsa_window* w, const void* q, const void* k, const voi
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool f16 = w->dtype == VSA_DTYPE_F16;
   float* part = static_cast<float*>(workspace);
-  if (w->d == 128) return f16 ? launch_fwd<128, true>(a, splits, part, st) : launch_fwd<128, false>(a, splits, part, st);
-  return f16 ? launch_fwd<64, true>(a, splits, part, st) : launch_fwd<64, false>(a, splits, part, st);
+  if (w->d == 128) return f16 ? launch_any<128, true>(a, plan, part, st) : launch_any<128, false>(a, plan, part, st);
+  return f16 ? launch_any<64, true>(a, plan, part, st) : launch_any<64, false>(a, plan, part, st);
 }
 
 size_t vsa_window_attn_bwd_workspace_bytes(const vsa_window* w) {
