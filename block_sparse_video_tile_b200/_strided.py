@@ -46,10 +46,6 @@ def strides(x: torch.Tensor, layout: str):
     return s[b], s[n], s[h]
 
 
-def new_heads(B: int, N: int, H: int, d: int, layout: str, dtype, device) -> torch.Tensor:
-    return torch.empty((B, H, N, d) if layout == "bhnd" else (B, N, H, d), dtype=dtype, device=device)
-
-
 def _span(x: torch.Tensor):
     """First and last-plus-one byte of a tensor."""
     n = sum((e - 1) * s for e, s in zip(x.shape, x.stride()))
@@ -96,9 +92,30 @@ class _Here:
         return False
 
 
+# The handle of a device's current stream, without an object around it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def on(device, stream, tensors):
     """Context of a call on the tensors' device and the given stream (None: that device's current one); its value
     is the stream handle.  Inputs and outputs on a given stream are kept until it is done with them."""
     if stream is None and device.index == torch.cuda.current_device():
-        return _Here(torch.cuda.current_stream(device).cuda_stream)
+        return _Here(_raw_stream(device.index))
     return _other(device, stream, tensors)
+
+
+def sig(x):
+    """What the checks of a call look at in a tensor: shape, strides, type and device (never its address)."""
+    return None if x is None else (x.shape, x.stride(), x.dtype, x.get_device())
+
+
+class Plans(dict):
+    """Checked argument structures by the signatures of a call's tensors and its other arguments; a call copies its
+    structure and fills in the addresses.  Emptied when it has grown large."""
+
+    def keep(self, key, plan):
+        if len(self) >= 512:
+            self.clear()
+        self[key] = plan
+        return plan

@@ -2,12 +2,10 @@
 (vsa_qk_norm_rope of include/vsa.h): what a video transformer's layer does to q and k before its attention."""
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
 from ._native import VsaNormRope, VsaQkSide, check, lib
-from ._strided import DTYPES, apart, dims, head_tensor, new_heads, on, strides
+from ._strided import AXES, DTYPES, Plans, apart, dims, head_tensor, on, sig, strides
 
 __all__ = ["rope_split", "rope_table", "qk_norm_rope", "qk_norm_rope_bwd"]
 
@@ -31,42 +29,67 @@ def rope_table(grid, d: int, *, split=None, theta: float = 10000.0, first=(0, 0,
     return torch.cat(parts).float()
 
 
-def _table(name, table, grid, split, device):
+def _check_table(name, table, grid, split, device):
     if table is None:
-        return 0
+        return
     rows = sum(n * (s // 2) for n, s in zip(grid, split))
     if not (table.device == device and table.dtype is torch.float32 and table.is_contiguous()
             and tuple(table.shape) == (rows, 2)):
         raise ValueError(f"{name} must be a contiguous float32 tensor of shape {(rows, 2)} on {device}")
-    return table.data_ptr()
 
 
-def _weight(name, w, d, dtype, device):
+def _check_weight(name, w, d, dtype, device):
     if w is None:
-        return 0, 0
+        return
     if not (w.device == device and w.dtype in (dtype, torch.float32) and w.shape == (d,) and w.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous [{d}] tensor of type {dtype} or float32 on {device}")
-    return w.data_ptr(), int(w.dtype is torch.float32)
 
 
-def _common(q, k, grid, grid_k, split, eps, interleaved, layout):
-    B, N, H, d = dims("q", q, layout)
+_PLANS = Plans()
+
+
+def _plan(key, q, k, grid, grid_k, split, eps, interleaved, layout, table, table_k, q_weight, k_weight, dy):
+    """(vsa_norm_rope, for q and k (vsa_qk_side without addresses, shape of a result), backward workspace bytes) of
+    checked arguments.  dy: gradients of the results for the backward call, else None."""
+    plan = _PLANS.get(key)
+    if plan is not None:
+        return plan
+    _, _, _, d = dims("q", q, layout)
     if q.dtype not in DTYPES:
         raise ValueError(f"q must be bfloat16 or float16, got {q.dtype}")
-    grid_k = grid if grid_k is None else grid_k
-    split = rope_split(d) if split is None else split
-    for name, x, g in (("q", q, grid), ("k", k, grid_k)):
+    device, dtype = q.device, q.dtype
+    split = rope_split(d) if split is None else tuple(split)
+    if k is not None and table is not None and table_k is None and grid_k != grid:
+        raise ValueError("keys on their own grid need table_k")
+    p = VsaNormRope(d, DTYPES[dtype], int(bool(interleaved)), split, eps)
+    sides = []
+    for name, x, g, t, w, gy in (("q", q, grid, table, q_weight, dy and dy[0]),
+                                 ("k", k, grid_k, table if table_k is None else table_k, k_weight, dy and dy[1])):
         if x is None:
+            sides.append(None)
             continue
         if len(g) != 3:
             raise ValueError("a grid is (T, Hh, W)")
-        head_tensor(name, x, None, layout, q.dtype, q.device)
-        b, n, _, dd = dims(name, x, layout)
-        if (n, dd) != (g[0] * g[1] * g[2], d):
-            raise ValueError(f"{name} has {n} tokens of {dd} channels, the grid {tuple(g)} and q ask for "
+        head_tensor(name, x, None, layout, dtype, device)
+        B, N, H, dd = dims(name, x, layout)
+        if (N, dd) != (g[0] * g[1] * g[2], d):
+            raise ValueError(f"{name} has {N} tokens of {dd} channels, the grid {g} and q ask for "
                              f"{g[0] * g[1] * g[2]} of {d}")
-    p = VsaNormRope(d, DTYPES[q.dtype], int(bool(interleaved)), tuple(split), eps)
-    return p, grid_k, split
+        if dy is not None:
+            head_tensor(f"d{name}_out", gy, (B, N, H, d), layout, dtype, device)
+        _check_table("table", t, g, split, device)
+        _check_weight(name + "_weight", w, d, dtype, device)
+        shape = (B, H, N, d) if layout == "bhnd" else (B, N, H, d)
+        new = strides(torch.empty(shape, device="meta"), layout)
+        side = VsaQkSide(B, H, *g, int(w is not None and w.dtype is torch.float32), 0, strides(x, layout), 0,
+                         new if dy is None else strides(gy, layout), 0, new, 0, 0, 0)
+        sides.append((side, shape) if B and N and H else (None, shape))
+    return _PLANS.keep(key, (p, sides))
+
+
+def _key(q, k, grid, grid_k, split, eps, interleaved, layout, table, table_k, q_weight, k_weight, dy):
+    return (sig(q), sig(k), grid, grid_k, None if split is None else tuple(split), eps, interleaved, layout, sig(table),
+            sig(table_k), sig(q_weight), sig(k_weight), None if dy is None else (sig(dy[0]), sig(dy[1])))
 
 
 def qk_norm_rope(q, k, grid, *, table=None, table_k=None, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -78,35 +101,42 @@ def qk_norm_rope(q, k, grid, *, table=None, table_k=None, q_weight=None, k_weigh
     and grid).  table: rope_table(grid, d, ...), None for no rotation; table_k: the keys' (default: table, when the
     keys have the queries' grid).  q_weight, k_weight: [d], the type of q or float32; None for ones.  interleaved: a
     pair is channels (2p, 2p + 1), else (p, p + d/2).  out: (q', k') to write to, apart from the inputs."""
-    p, grid_k, split = _common(q, k, grid, grid_k, split, eps, interleaved, layout)
-    device, dtype, d = q.device, q.dtype, p.d
-    if table_k is None and table is not None and k is not None:
-        if tuple(grid_k) != tuple(grid):
-            raise ValueError("keys on their own grid need table_k")
-        table_k = table
+    grid = tuple(grid)
+    args = (q, k, grid, grid if grid_k is None else tuple(grid_k), split, eps, interleaved, layout, table, table_k,
+            q_weight, k_weight, None)
+    p, sides = _plan(_key(*args), *args)
+    device = q.device
+    if out is not None:
+        for y, side in zip(out, sides):
+            if side is not None:
+                b, n, h = AXES[layout]
+                s = side[1]
+                head_tensor("out", y, (s[b], s[n], s[h], s[3]), layout, q.dtype, device)
+        apart([("out", y) for y in out if y is not None],
+              [(n, x) for n, x in (("q", q), ("k", k), ("table", table), ("q_weight", q_weight), ("k_weight", k_weight))
+               if x is not None])
     with on(device, stream, (q, k, table, table_k, q_weight, k_weight) + tuple(out or ())) as st:
-        sides, outs = [], []
-        for i, (name, x, g, t, w) in enumerate((("q", q, grid, table, q_weight), ("k", k, grid_k, table_k, k_weight))):
-            if x is None:
+        call, outs = [], []
+        for i, (side, x, t, w) in enumerate(((sides[0], q, table, q_weight),
+                                             (sides[1], k, table if table_k is None else table_k, k_weight))):
+            if side is None:
                 outs.append(None)
                 continue
-            B, N, H, _ = dims(name, x, layout)
-            if out is None:
-                y = new_heads(B, N, H, d, layout, dtype, device)
-            else:
-                y = out[i]
-                head_tensor("out", y, (B, N, H, d), layout, dtype, device)
-            wp, wf = _weight(name + "_weight", w, d, dtype, device)
+            y = x.new_empty(side[1]) if out is None else out[i]
             outs.append(y)
-            if B and N and H:
-                sides.append(VsaQkSide(B, H, *g, wf, x.data_ptr(), strides(x, layout), y.data_ptr(), strides(y, layout),
-                                       0, (0, 0, 0), wp, _table("table", t, g, split, device), 0))
-        if out is not None:
-            apart([("out", o) for o in outs if o is not None],
-                  [(n, x) for n, x in (("q", q), ("k", k), ("table", table), ("q_weight", q_weight),
-                                       ("k_weight", k_weight)) if x is not None])
-        if sides:
-            check("vsa_qk_norm_rope", lib().vsa_qk_norm_rope(p, sides[0], sides[1] if len(sides) > 1 else None, st))
+            if side[0] is None:
+                continue
+            c = VsaQkSide.from_buffer_copy(side[0])
+            c.x, c.y = x.data_ptr(), y.data_ptr()
+            if out is not None:
+                c.y_s = strides(y, layout)
+            if w is not None:
+                c.weight = w.data_ptr()
+            if t is not None:
+                c.table = t.data_ptr()
+            call.append(c)
+        if call:
+            check("vsa_qk_norm_rope", lib().vsa_qk_norm_rope(p, call[0], call[1] if len(call) > 1 else None, st))
     return outs[0], outs[1]
 
 
@@ -115,36 +145,39 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, grid, *, table=None, table_k=None, q_
                      stream=None):
     """Gradient of qk_norm_rope: (dq, dk, dq_weight, dk_weight) from the gradients of its results and its inputs.
     The weights' gradients are float32 [d], None where the weight is None, summed in a fixed order."""
-    p, grid_k, split = _common(q, k, grid, grid_k, split, eps, interleaved, layout)
-    device, dtype, d = q.device, q.dtype, p.d
+    grid = tuple(grid)
     if (k is None) != (dk_out is None):
         raise ValueError("give k and dk_out, or neither")
-    if table_k is None and table is not None and k is not None:
-        if tuple(grid_k) != tuple(grid):
-            raise ValueError("keys on their own grid need table_k")
-        table_k = table
+    args = (q, k, grid, grid if grid_k is None else tuple(grid_k), split, eps, interleaved, layout, table, table_k,
+            q_weight, k_weight, (dq_out, dk_out))
+    p, sides = _plan(_key(*args), *args)
+    device = q.device
     with on(device, stream, (q, k, dq_out, dk_out, table, table_k, q_weight, k_weight)) as st:
-        sides, dx, dw = [], [], []
-        for name, x, dy, g, t, w in (("q", q, dq_out, grid, table, q_weight), ("k", k, dk_out, grid_k, table_k, k_weight)):
-            if x is None:
+        call, dx, dw = [], [], []
+        for side, x, dy, t, w in ((sides[0], q, dq_out, table, q_weight),
+                                  (sides[1], k, dk_out, table if table_k is None else table_k, k_weight)):
+            if side is None:
                 dx.append(None)
                 dw.append(None)
                 continue
-            B, N, H, _ = dims(name, x, layout)
-            head_tensor(f"d{name}_out", dy, (B, N, H, d), layout, dtype, device)
-            wp, wf = _weight(name + "_weight", w, d, dtype, device)
-            gx = new_heads(B, N, H, d, layout, dtype, device)
-            some = B and N and H
-            gw = None if w is None else (torch.empty if some else torch.zeros)(d, dtype=torch.float32, device=device)
+            gx = x.new_empty(side[1])
+            gw = None if w is None else torch.empty(p.d, dtype=torch.float32, device=device)
             dx.append(gx)
             dw.append(gw)
-            if some:
-                sides.append(VsaQkSide(B, H, *g, wf, x.data_ptr(), strides(x, layout), dy.data_ptr(),
-                                       strides(dy, layout), gx.data_ptr(), strides(gx, layout), wp,
-                                       _table("table", t, g, split, device), 0 if gw is None else gw.data_ptr()))
-        if sides:
-            sk = sides[1] if len(sides) > 1 else None
-            n = lib().vsa_qk_norm_rope_bwd_workspace_bytes(p, sides[0], sk)
+            if side[0] is None:
+                if gw is not None:
+                    gw.zero_()
+                continue
+            c = VsaQkSide.from_buffer_copy(side[0])
+            c.x, c.y, c.dx = x.data_ptr(), dy.data_ptr(), gx.data_ptr()
+            if w is not None:
+                c.weight, c.dweight = w.data_ptr(), gw.data_ptr()
+            if t is not None:
+                c.table = t.data_ptr()
+            call.append(c)
+        if call:
+            sk = call[1] if len(call) > 1 else None
+            n = lib().vsa_qk_norm_rope_bwd_workspace_bytes(p, call[0], sk)
             ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
-            check("vsa_qk_norm_rope_bwd", lib().vsa_qk_norm_rope_bwd(p, sides[0], sk, ws.data_ptr() if n else None, n, st))
+            check("vsa_qk_norm_rope_bwd", lib().vsa_qk_norm_rope_bwd(p, call[0], sk, ws.data_ptr() if n else None, n, st))
     return dx[0], dx[1], dw[0], dw[1]

@@ -7,11 +7,10 @@ import math
 import torch
 
 from ._native import VsaWindow, check, lib
-from ._strided import DTYPES, apart, dims, head_tensor, new_heads, on, strides
+from ._strided import AXES, DTYPES, Plans, apart, dims, head_tensor, on, sig, strides
 
 __all__ = ["window_attn", "window_attn_bwd"]
 
-_NO = (0, 0, 0)
 _MAX_POS = 1 << 30
 
 
@@ -28,9 +27,18 @@ def _positions(name, x, lo, hi, B, device):
     return torch.full((B,), int(x), dtype=torch.int32, device=device)
 
 
-def _common(q, k, v, window, sink, unit, layout, scale):
+_PLANS = Plans()
+
+
+def _plan(q, k, v, window, sink, unit, layout, scale, do=None, out=None, lse=None):
+    """(vsa_window without addresses, shape of O, shape of dK and dV, scale, workspace bytes) of checked arguments;
+    the backward call gives do, out and lse."""
+    key = (sig(q), sig(k), sig(v), window, sink, unit, layout, scale, sig(do), sig(out), sig(lse))
+    plan = _PLANS.get(key)
+    if plan is not None:
+        return plan
     B, Nq, Hq, d = dims("q", q, layout)
-    Bk, Nk, Hkv, _ = dims("k", k, layout)
+    _, Nk, Hkv, _ = dims("k", k, layout)
     if q.dtype not in DTYPES:
         raise ValueError(f"q must be bfloat16 or float16, got {q.dtype}")
     device, dtype = q.device, q.dtype
@@ -40,7 +48,29 @@ def _common(q, k, v, window, sink, unit, layout, scale):
     for name, x, lo in (("window", window, 1), ("sink", sink, 0), ("unit", unit, 1)):
         if not lo <= x < 1 << 31:
             raise ValueError(f"{name} must be at least {lo} (and fit 32 bits), got {x}")
-    return B, Nq, Hq, d, Nk, Hkv, 1.0 / math.sqrt(d) if scale is None else scale
+    oshape = (B, Hq, Nq, d) if layout == "bhnd" else (B, Nq, Hq, d)
+    kshape = (B, Hkv, Nk, d) if layout == "bhnd" else (B, Nk, Hkv, d)
+    no, nk = (strides(torch.empty(x, device="meta"), layout) for x in (oshape, kshape))
+    if do is not None:
+        head_tensor("do", do, (B, Nq, Hq, d), layout, dtype, device)
+        head_tensor("out", out, (B, Nq, Hq, d), layout, dtype, device)
+        _check_lse(lse, (B, Hq, Nq), device)
+    w = VsaWindow(B, Hq, Hkv, Nq, Nk, d, DTYPES[dtype], window, sink, unit, 0, 0, strides(q, layout), strides(k, layout),
+                  strides(v, layout), no if do is None else strides(out, layout), no if do is None else strides(do, layout),
+                  no, nk, nk)
+    size = 0
+    if B and Nq and Hq and Nk and Hkv:
+        size = (lib().vsa_window_attn_workspace_bytes if do is None else lib().vsa_window_attn_bwd_workspace_bytes)(w)
+    return _PLANS.keep(key, (w, oshape, kshape, 1.0 / math.sqrt(d) if scale is None else scale, size))
+
+
+def _check_lse(lse, shape, device):
+    if not (lse.device == device and lse.dtype is torch.float32 and lse.is_contiguous() and tuple(lse.shape) == shape):
+        raise ValueError(f"lse must be a contiguous float32 tensor of shape {shape} on {device}")
+
+
+def _tensor(x):
+    return x if isinstance(x, torch.Tensor) else None
 
 
 def window_attn(q, k, v, window: int, *, sink: int = 0, unit: int = 1, kv_len=None, q_start=None,
@@ -54,36 +84,36 @@ def window_attn(q, k, v, window: int, *, sink: int = 0, unit: int = 1, kv_len=No
     anything.  q_start: position of the first query (default kv_len - Nq: the queries are the last tokens).  A query
     that sees nothing gets O = 0 and LSE = -inf.  O is like q, LSE float32 [B, Hq, Nq]; both can be given, apart from
     the inputs."""
-    B, Nq, Hq, d, Nk, Hkv, scale = _common(q, k, v, window, sink, unit, layout, scale)
-    device = q.device
-    with on(device, stream, (q, k, v, kv_len if isinstance(kv_len, torch.Tensor) else None,
-                             q_start if isinstance(q_start, torch.Tensor) else None, out, lse)) as st:
+    t, oshape, _, scale, size = _plan(q, k, v, window, sink, unit, layout, scale)
+    device, B, Nk = q.device, t.B, t.Nk
+    if out is not None or lse is not None:
+        if out is not None:
+            b, n, h = AXES[layout]
+            head_tensor("out", out, (oshape[b], oshape[n], oshape[h], oshape[3]), layout, q.dtype, device)
+        if lse is not None:
+            _check_lse(lse, (B, t.Hq, t.Nq), device)
+        apart([(name, x) for name, x in (("out", out), ("lse", lse)) if x is not None], [("q", q), ("k", k), ("v", v)])
+    with on(device, stream, (q, k, v, _tensor(kv_len), _tensor(q_start), out, lse)) as st:
         n = _positions("kv_len", kv_len, 0, Nk, B, device)
         p0 = _positions("q_start", q_start, -_MAX_POS, _MAX_POS, B, device)
-        given = [(name, x) for name, x in (("out", out), ("lse", lse)) if x is not None]
+        w = VsaWindow.from_buffer_copy(t)
         if out is None:
-            out = new_heads(B, Nq, Hq, d, layout, q.dtype, device)
+            out = q.new_empty(oshape)
         else:
-            head_tensor("out", out, (B, Nq, Hq, d), layout, q.dtype, device)
+            w.o_s = strides(out, layout)
         if lse is None:
-            lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=device)
-        elif not (lse.device == device and lse.dtype is torch.float32 and lse.is_contiguous()
-                  and tuple(lse.shape) == (B, Hq, Nq)):
-            raise ValueError(f"lse must be a contiguous float32 tensor of shape {(B, Hq, Nq)} on {device}")
-        if given:
-            apart(given, [("q", q), ("k", k), ("v", v)])
-        if not (B and Nq and Hq):
+            lse = torch.empty((B, w.Hq, w.Nq), dtype=torch.float32, device=device)
+        if not (B and w.Nq and w.Hq):
             return out, lse
-        if not (Nk and Hkv):
+        if not (Nk and w.Hkv):
             return out.zero_(), lse.fill_(-math.inf)
-        w = VsaWindow(B, Hq, Hkv, Nq, Nk, d, DTYPES[q.dtype], window, sink, unit, 0 if n is None else n.data_ptr(),
-                      0 if p0 is None else p0.data_ptr(), strides(q, layout), strides(k, layout), strides(v, layout),
-                      strides(out, layout), _NO, _NO, _NO, _NO)
-        size = lib().vsa_window_attn_workspace_bytes(w)
-        ws = torch.empty(size, dtype=torch.uint8, device=device) if size else None
+        if n is not None:
+            w.kv_len = n.data_ptr()
+        if p0 is not None:
+            w.q_start = p0.data_ptr()
+        ws = torch.empty(size, dtype=torch.uint8, device=device).data_ptr() if size else None
         check("vsa_window_attn", lib().vsa_window_attn(
-            w, q.data_ptr(), k.data_ptr(), v.data_ptr(), scale, out.data_ptr(), lse.data_ptr(),
-            ws.data_ptr() if size else None, size, st))
+            w, q.data_ptr(), k.data_ptr(), v.data_ptr(), scale, out.data_ptr(), lse.data_ptr(), ws, size, st))
     return out, lse
 
 
@@ -92,28 +122,21 @@ def window_attn_bwd(do, q, k, v, out, lse, window: int, *, sink: int = 0, unit: 
     """Gradient of window_attn: (dq, dk, dv) from the gradient of O, the inputs and the (O, LSE) that it gave, with
     the same window.  A key/value head's gradient is the sum over its query heads; keys that no query sees get
     zeros.  Every sum has a fixed order (the same bits each time)."""
-    B, Nq, Hq, d, Nk, Hkv, scale = _common(q, k, v, window, sink, unit, layout, scale)
-    device, dtype = q.device, q.dtype
-    head_tensor("do", do, (B, Nq, Hq, d), layout, dtype, device)
-    head_tensor("out", out, (B, Nq, Hq, d), layout, dtype, device)
-    if not (lse.device == device and lse.dtype is torch.float32 and lse.is_contiguous()
-            and tuple(lse.shape) == (B, Hq, Nq)):
-        raise ValueError(f"lse must be a contiguous float32 tensor of shape {(B, Hq, Nq)} on {device}")
-    with on(device, stream, (do, q, k, v, out, lse, kv_len if isinstance(kv_len, torch.Tensor) else None,
-                             q_start if isinstance(q_start, torch.Tensor) else None)) as st:
-        n = _positions("kv_len", kv_len, 0, Nk, B, device)
+    t, oshape, kshape, scale, size = _plan(q, k, v, window, sink, unit, layout, scale, do, out, lse)
+    device, B = q.device, t.B
+    with on(device, stream, (do, q, k, v, out, lse, _tensor(kv_len), _tensor(q_start))) as st:
+        n = _positions("kv_len", kv_len, 0, t.Nk, B, device)
         p0 = _positions("q_start", q_start, -_MAX_POS, _MAX_POS, B, device)
-        dq = new_heads(B, Nq, Hq, d, layout, dtype, device)
-        dk, dv = (new_heads(B, Nk, Hkv, d, layout, dtype, device) for _ in range(2))
-        if not (B and Nq and Hq and Nk and Hkv):
+        dq, dk, dv = q.new_empty(oshape), k.new_empty(kshape), k.new_empty(kshape)
+        if not (B and t.Nq and t.Hq and t.Nk and t.Hkv):
             return dq.zero_(), dk.zero_(), dv.zero_()
-        w = VsaWindow(B, Hq, Hkv, Nq, Nk, d, DTYPES[dtype], window, sink, unit, 0 if n is None else n.data_ptr(),
-                      0 if p0 is None else p0.data_ptr(), strides(q, layout), strides(k, layout), strides(v, layout),
-                      strides(out, layout), strides(do, layout), strides(dq, layout), strides(dk, layout),
-                      strides(dv, layout))
-        size = lib().vsa_window_attn_bwd_workspace_bytes(w)
-        ws = torch.empty(size, dtype=torch.uint8, device=device) if size else None
+        w = VsaWindow.from_buffer_copy(t)
+        if n is not None:
+            w.kv_len = n.data_ptr()
+        if p0 is not None:
+            w.q_start = p0.data_ptr()
+        ws = torch.empty(size, dtype=torch.uint8, device=device)
         check("vsa_window_attn_bwd", lib().vsa_window_attn_bwd(
             w, do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), scale,
-            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr() if size else None, size, st))
+            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), size, st))
     return dq, dk, dv
