@@ -26,12 +26,12 @@ int take_strides(const int64_t in[3], int B, int N, int H, int d, long long out[
   return VSA_OK;
 }
 
-// CTAs of a backward launch per side: enough to fill the GPU twice over (each
-// leaves one partial sum of dweight, so their number is bounded).
-constexpr int kNrBwdCtas = 148 * 4;
-// A CTA walks all heads of its tokens once there are this many CTAs without
-// splitting them; below it the heads are split into chunks of kNrRows.
-constexpr int kNrWantCtas = 148 * 8;
+// CTAs of a launch, both sides together: two an SM (each backward CTA leaves
+// one partial sum of dweight).
+constexpr int kNrCtas = 148 * 2;
+// A CTA walks all heads of its tokens if that gives this many items a side;
+// below it the heads are split into chunks of kNrChunk or more.
+constexpr int kNrWantItems = 148 * 8;
 
 static int nr_side(const vsa_norm_rope* p, const vsa_qk_side* in, bool bwd, NrSide* s) {
   if (in->B <= 0 || in->H <= 0 || in->T <= 0 || in->Hh <= 0 || in->W <= 0) return VSA_ERR_INVALID_ARG;
@@ -62,15 +62,18 @@ static int nr_side(const vsa_norm_rope* p, const vsa_qk_side* in, bool bwd, NrSi
   s->toff1 = static_cast<int>(1ll * in->T * (p->split[0] / 2));
   s->toff2 = static_cast<int>(rows);
   s->partial = nullptr;
-  const int tok = kNrThreads / (p->d / 8);
+  const int lane_groups = 512 / p->d;                  // of a warp
+  s->across = s->xs[2] < s->xs[1] && in->H >= kNrRows * lane_groups;
+  const int tok = kNrThreads / 32 * (s->across ? 1 : lane_groups);
   s->groups = (s->N + tok - 1) / tok;
   const long long whole = 1ll * in->B * s->groups;
   s->chunks = 1;
-  if (whole < kNrWantCtas) {
-    const long long most = (in->H + kNrRows - 1) / kNrRows;
-    s->chunks = static_cast<int>(std::min<long long>(most, (kNrWantCtas + whole - 1) / whole));
+  const int least = s->across ? kNrRows * lane_groups : kNrChunk;
+  if (whole < kNrWantItems) {
+    const long long most = (in->H + least - 1) / least;
+    s->chunks = static_cast<int>(std::min<long long>(most, (kNrWantItems + whole - 1) / whole));
   }
-  s->hpc = (in->H + s->chunks - 1) / s->chunks;
+  s->hpc = ((in->H + s->chunks - 1) / s->chunks + least - 1) / least * least;
   s->chunks = (in->H + s->hpc - 1) / s->hpc;
   if (whole * s->chunks > (1ll << 30)) return VSA_ERR_TOO_LARGE;   // the kernel's item index steps by the grid in 32 bits
   s->items = static_cast<int>(whole * s->chunks);
@@ -99,11 +102,23 @@ static int nr_args(const vsa_norm_rope* p, const vsa_qk_side* q, const vsa_qk_si
   return k != nullptr ? nr_side(p, k, bwd, &a->s[1]) : VSA_OK;
 }
 
+// CTAs a side (grid.x).
+static int nr_ctas(const NrArgs& a) {
+  return std::min(a.s[1].items > 0 ? kNrCtas / 2 : kNrCtas, std::max(a.s[0].items, a.s[1].items));
+}
+
 template <bool BWD>
 static int nr_launch(const vsa_norm_rope* p, const NrArgs& a, int ctas, int sides, cudaStream_t st) {
   const dim3 grid(ctas, sides);
   const bool f16 = p->dtype == VSA_DTYPE_F16, il = p->interleaved != 0;
-#define VSA_NR(D, F, I) norm_rope_kernel<D, F, I, BWD><<<grid, kNrThreads, 0, st>>>(a)
+  constexpr int smem = nr_smem_bytes<BWD>();
+#define VSA_NR(D, F, I)                                                                                        \
+  do {                                                                                                         \
+    if (cudaFuncSetAttribute(norm_rope_kernel<D, F, I, BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != \
+        cudaSuccess)                                                                                           \
+      return VSA_ERR_CUDA;                                                                                     \
+    norm_rope_kernel<D, F, I, BWD><<<grid, kNrThreads, smem, st>>>(a);                                         \
+  } while (0)
   if (p->d == 128) {
     if (f16) { if (il) VSA_NR(128, true, true); else VSA_NR(128, true, false); }
     else { if (il) VSA_NR(128, false, true); else VSA_NR(128, false, false); }
@@ -115,11 +130,10 @@ static int nr_launch(const vsa_norm_rope* p, const NrArgs& a, int ctas, int side
   return cudaGetLastError() == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
 }
 
-static int nr_bwd_ctas(const NrArgs& a) { return std::min(kNrBwdCtas, std::max(a.s[0].items, a.s[1].items)); }
 
 static size_t nr_bwd_bytes(const vsa_norm_rope* p, const NrArgs& a, const vsa_qk_side* q, const vsa_qk_side* k) {
   const size_t sides = (q->weight != nullptr ? 1 : 0) + (k != nullptr && k->weight != nullptr ? 1 : 0);
-  return sides * nr_bwd_ctas(a) * p->d * sizeof(float);
+  return sides * nr_ctas(a) * p->d * sizeof(float);
 }
 
 }  // namespace vsa
@@ -133,8 +147,7 @@ int vsa_qk_norm_rope(const vsa_norm_rope* p, const vsa_qk_side* q, const vsa_qk_
   int rc = nr_args(p, q, k, false, &a);
   if (rc != VSA_OK) return rc;
   if ((rc = check_arch()) != VSA_OK) return rc;
-  return nr_launch<false>(p, a, std::max(a.s[0].items, a.s[1].items), k != nullptr ? 2 : 1,
-                          static_cast<cudaStream_t>(stream));
+  return nr_launch<false>(p, a, nr_ctas(a), k != nullptr ? 2 : 1, static_cast<cudaStream_t>(stream));
 }
 
 size_t vsa_qk_norm_rope_bwd_workspace_bytes(const vsa_norm_rope* p, const vsa_qk_side* q, const vsa_qk_side* k) {
@@ -152,7 +165,7 @@ int vsa_qk_norm_rope_bwd(const vsa_norm_rope* p, const vsa_qk_side* q, const vsa
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return VSA_ERR_WORKSPACE;
   if ((rc = check_arch()) != VSA_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int ctas = nr_bwd_ctas(a);
+  const int ctas = nr_ctas(a);
   float* ws = static_cast<float*>(workspace);
   if (q->weight != nullptr) {
     a.s[0].partial = ws;
