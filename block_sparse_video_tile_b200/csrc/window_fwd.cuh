@@ -17,11 +17,22 @@
 // TMEM lane), 8 loads Q and K, 9 loads V, 10 and 11 issue the MMAs of slot 0
 // and 1 (an issuer each: a thread that has queued MMAs sees its next barrier
 // test late).  TMEM: S0, S1 (128 columns each), O0, O1 (D each).  P, packed to
-// 16 bits, overwrites the first half of its slot's S in two halves of 64 keys,
-// each released to the P V MMAs as soon as it is stored; S of the slot's next
-// block follows P V in the issue order, so S_FULL also says that P V of the
-// block before is complete and O may be rescaled (only when a row's maximum
-// grew by more than 2^8).
+// 16 bits, overwrites the first half of its slot's S, 32 keys at a time, and is
+// released to the P V MMAs in three parts; S of the slot's next block is
+// queued right behind P V, so S_FULL also says that P V of the block before is
+// complete and O may be rescaled (only when a row's maximum grew by more than
+// 2^8).
+//
+// A block's cycle (clock stamps, d = 128): scores seen, 90 clk to load them,
+// 560 for the maximum and the first 32 keys' P, 3 x 540 for the others, then
+// the last P V and the next S: 3.4-3.7k clk for two 128 x 128 blocks (2048 of
+// MMA).  window_wan5b (6 heads of 27280 tokens, 8 frames and a sink): 575 us in
+// bursts (1005 TFLOP/s, 62 % of the measured peak), 600 us under the power cap.
+// Measured and not taken: a warpgroup on each half of a block's keys (four
+// softmax warps a sub-partition, row maxima joined by an OR barrier) 8 %
+// slower; 1/8 to 3/8 of the exponentials on the FMA pipe 4 to 10 % slower; the
+// maximum before any exponential, P released in halves and the next S issued
+// after a K wait 8 % slower.
 //
 // Rounding: P is rounded to the 16-bit input type for the P V MMA (its sum l
 // is taken from the float32 values), O once at the end.
@@ -40,10 +51,6 @@ constexpr int kWfKeys = 128;             // keys a block
 constexpr int kWfRegSoftmax = 208, kWfRegOther = 88;
 static_assert(2 * 128 * kWfRegSoftmax + 128 * kWfRegOther <= kWfThreads * 168, "register split over the launch budget");
 constexpr float kWfRescaleLog2 = 8.0f;
-#ifndef VSA_WIN_POLY_PER8
-#define VSA_WIN_POLY_PER8 0
-#endif
-
 template <int D>
 struct WfSmem {
   static constexpr int kSlab = 128 * 128;              // 128 rows x 64 channels
@@ -59,9 +66,10 @@ struct WfSmem {
   static constexpr int kTotal = kMisc + 16 + 1024;     // 1024: alignment of the base
 };
 
+// P of a block is released in three parts: keys 0-63, 64-95, 96-127.
 enum : int {
-  WB_Q = 0, WB_S = 1 /* [slot] */, WB_P = 3 /* [slot][half] */, WB_O = 7 /* [slot] */, WB_DRAIN = 9,
-  WB_K_FULL = 10, WB_K_EMPTY = 14, WB_V_FULL = 18, WB_V_EMPTY = 22
+  WB_Q = 0, WB_S = 1 /* [slot] */, WB_P = 3 /* [slot][3] */, WB_O = 9 /* [slot] */, WB_DRAIN = 11,
+  WB_K_FULL = 12, WB_K_EMPTY = 16, WB_V_FULL = 20, WB_V_EMPTY = 24
 };
 
 // Blocks of 128 keys that rows i0 .. i1 (inclusive) of a sequence see: ns
@@ -97,13 +105,14 @@ __device__ __forceinline__ WinBlocks win_blocks(const WinArgs& a, int len, int s
   return w;
 }
 
+// Mask of the 32 keys from c0 for one row.
+__device__ __forceinline__ uint32_t vis_word(const RowVis& v, int c0) {
+  return (low_bits(v.hi - c0) & ~low_bits(v.lo - c0)) | low_bits(v.first - c0);
+}
 // Mask words of the 128 keys from c0 for one row.
 __device__ __forceinline__ void vis_words(const RowVis& v, int c0, uint32_t (&m)[4]) {
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const int base = c0 + 32 * w;
-    m[w] = (low_bits(v.hi - base) & ~low_bits(v.lo - base)) | low_bits(v.first - base);
-  }
+  for (int w = 0; w < 4; ++w) m[w] = vis_word(v, c0 + 32 * w);
 }
 
 // splits > 1: blockIdx.z = batch * splits + split; a split takes its share of
@@ -137,7 +146,7 @@ __global__ void __launch_bounds__(kWfThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
       uint32_t cnt = 1;
-      if (i >= WB_P && i < WB_P + 4) cnt = 128;
+      if (i >= WB_P && i < WB_P + 6) cnt = 128;
       if (i == WB_DRAIN || (i >= WB_K_EMPTY && i < WB_K_EMPTY + 4) || (i >= WB_V_EMPTY && i < WB_V_EMPTY + 4)) cnt = 2;
       mbar_init(bar(i), cnt);
     }
@@ -213,47 +222,71 @@ __global__ void __launch_bounds__(kWfThreads, 1)
       }
       return j;
     };
+    auto wait_k = [&](int j) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(WB_K_FULL + j % L::kKSt), (j / L::kKSt) & 1, abort_flag, a.err));
+    };
+    // (elected lane) S of block j over the slot's score columns
     auto scores = [&](int j) {
       const int ks = j % L::kKSt;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(WB_K_FULL + ks), (j / L::kKSt) & 1, abort_flag, a.err));
-      if (!ok) return;
-      tc_fence_after();
-      if (elect_one_sync()) {
-        const uint32_t kb = base + L::kK + ks * L::kBuf;
+      const uint32_t kb = base + L::kK + ks * L::kBuf;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const int off = (kk / 4) * L::kSlab + (kk % 4) * 32;
-          mma_ss(tS, smem_desc_sw128(sQ + off, 16, 1024), smem_desc_sw128(kb + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
-        }
-        mma_commit(bar(WB_S + s));
-        mma_commit(bar(WB_K_EMPTY + ks));
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const int off = (kk / 4) * L::kSlab + (kk % 4) * 32;
+        mma_ss(tS, smem_desc_sw128(sQ + off, 16, 1024), smem_desc_sw128(kb + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
       }
-      __syncwarp();
+      mma_commit(bar(WB_S + s));
+      mma_commit(bar(WB_K_EMPTY + ks));
     };
     int j = skip(0), c = 0;
-    if (ok && j < n) scores(j);
+    if (ok && j < n) {
+      wait_k(j);
+      if (ok) {
+        tc_fence_after();
+        if (elect_one_sync()) scores(j);
+        __syncwarp();
+      }
+    }
     while (ok && j < n) {
       const int vs = j % L::kVSt;
       const uint32_t vb = base + L::kV + vs * L::kBuf;
+      // S of the next block is queued right behind this block's last P V: its
+      // K is waited for before, since a thread's barrier test behind queued
+      // MMAs waits for them to drain.  Not across blocks that are skipped
+      // (their V stage may be this block's, which is not released yet).
+      const bool next = j + 1 < n && mine.has(wb.block(it0 + j + 1));
       ok = __all_sync(0xffffffffu, mbar_wait(bar(WB_V_FULL + vs), (j / L::kVSt) & 1, abort_flag, a.err));
 #pragma unroll
-      for (int hf = 0; hf < 2 && ok; ++hf) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(WB_P + 2 * s + hf), c & 1, abort_flag, a.err));
+      for (int pt = 0; pt < 3 && ok; ++pt) {
+        if (pt == 1 && next) wait_k(j + 1);
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(WB_P + 3 * s + pt), c & 1, abort_flag, a.err));
         if (!ok) break;
         tc_fence_after();
         if (elect_one_sync()) {
 #pragma unroll
-          for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk)          // 16 keys = 16 rows of 128 bytes
+          for (int kk = pt == 0 ? 0 : 2 + 2 * pt; kk < 4 + 2 * pt; ++kk)    // 16 keys = 16 rows of 128 bytes
             mma_ts(tO, tS + 8u * kk, smem_desc_sw128(vb + kk * 2048, L::kSlab, 1024), idPV,
                    (c > 0 || kk > 0) ? 1u : 0u);
-          if (hf == 1) mma_commit(bar(WB_V_EMPTY + vs));
+          if (pt == 2) {
+            if (next) scores(j + 1);
+            mma_commit(bar(WB_V_EMPTY + vs));
+          }
         }
         __syncwarp();
       }
       ++c;
       if (!ok) break;
+      if (next) {
+        ++j;
+        continue;
+      }
       j = skip(j + 1);
-      if (ok && j < n) scores(j);
+      if (ok && j < n) {
+        wait_k(j);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one_sync()) scores(j);
+        __syncwarp();
+      }
     }
     if (elect_one_sync()) {
       if (c > 0) mma_commit(bar(WB_O + s));
@@ -308,6 +341,7 @@ __global__ void __launch_bounds__(kWfThreads, 1)
       tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&x[64]));
       tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&x[96]));
       tmem_wait_ld();
+      sched_fence(a);
       if (masked) {
         uint32_t mw[4];
         vis_words(vis, c0, mw);
@@ -321,49 +355,58 @@ __global__ void __launch_bounds__(kWfThreads, 1)
 #pragma unroll
       for (int e = 4; e < 128; e += 2)
         mx4[(e >> 1) & 3] = fmax3(mx4[(e >> 1) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+      // P of the first 32 keys against the reference as it stands, made while
+      // the maximum is; kept unless the maximum moves the reference.
+      uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
+      auto expo = [&](int at, uint64_t nm2, uint32_t* pk) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint64_t z2 = f2_fma(f2_pack(__uint_as_float(x[at + 2 * e]), __uint_as_float(x[at + 2 * e + 1])), sc2, nm2);
+          float z0, z1;
+          f2_unpack(z2, z0, z1);
+          const float p0 = ex2_approx(z0), p1 = ex2_approx(z1);
+          ls2[e & 3] = f2_add(ls2[e & 3], f2_pack(p0, p1));
+          pk[e] = pack_elem2<F16>(p0, p1);
+        }
+      };
+      uint32_t pk[16];
+      float mu = m == -INFINITY ? 0.f : m;
+      expo(0, f2_pack(-mu, -mu), pk);
       const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
-      const float m_new = mx > m + kWfRescaleLog2 ? mx : m;
-      const float mu = m_new == -INFINITY ? 0.f : m_new;
-      const uint64_t nm2 = f2_pack(-mu, -mu);
-      if (__any_sync(0xffffffffu, m_new != m)) {
+      sched_fence(a);
+      if (__any_sync(0xffffffffu, mx > m + kWfRescaleLog2)) {
+        const float m_new = mx > m + kWfRescaleLog2 ? mx : m;
         const float f = m_new == m ? 1.f : (m == -INFINITY ? 0.f : ex2_approx(m - m_new));
         l *= f;
+        m = m_new;
         if (c > 0) {
           // P V of the slot's block before is complete (S_FULL), so O is still
 #pragma unroll
-          for (int q4 = 0; q4 < D / 32; ++q4) {
-            uint32_t ov[32];
-            tmem_ld32(tO + 32u * q4, ov);
+          for (int q = 0; q < D / 16; ++q) {
+            uint32_t ov[16];
+            tmem_ld16(tO + 16u * q, ov);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
-            tmem_st32(tO + 32u * q4, ov);
+            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
+            tmem_st16(tO + 16u * q, ov);
           }
         }
-        m = m_new;
+        mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ls2[e] = 0ull;
+        expo(0, f2_pack(-mu, -mu), pk);
       }
-      uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
+      const uint64_t nm2 = f2_pack(-mu, -mu);
+      sched_fence(a);
+      tmem_st16(tS, pk);
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-        for (int e = 32 * hf; e < 32 * hf + 32; ++e) {
-          const uint64_t z2 = f2_fma(f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sc2, nm2);
-          float p0, p1;
-          if ((e & 7) < VSA_WIN_POLY_PER8) {
-            exp2_poly_pair(z2, p0, p1);
-          } else {
-            float z0, z1;
-            f2_unpack(z2, z0, z1);
-            p0 = ex2_approx(z0);
-            p1 = ex2_approx(z1);
-          }
-          ls2[e & 3] = f2_add(ls2[e & 3], f2_pack(p0, p1));
-          x[e] = pack_elem2<F16>(p0, p1);
-        }
-        tmem_st32(tS + 32u * hf, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * hf]));
+      for (int q = 1; q < 4; ++q) {
+        expo(32 * q, nm2, pk);
+        tmem_st16(tS + 16u * q, pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar(WB_P + 2 * s + hf));
+        mbar_arrive(bar(WB_P + 3 * s + q - 1));
+        sched_fence(a);
       }
       float s0, s1;
       f2_unpack(f2_add(f2_add(ls2[0], ls2[1]), f2_add(ls2[2], ls2[3])), s0, s1);

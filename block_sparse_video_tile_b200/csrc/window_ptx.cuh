@@ -3,6 +3,7 @@
 #pragma once
 
 #include "vsa_ptx.cuh"
+#include "window_args.cuh"
 
 namespace vsa {
 
@@ -32,6 +33,23 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// A branch that is never taken (units are positive).  It ends a basic block, so
+// the compiler keeps the work of the chunks around it apart; without it the
+// chunks' exponentials are interleaved and every store of P comes late
+// (window_wan5b 675 us instead of 575).
+__device__ __forceinline__ void sched_fence(const WinArgs& a) {
+  if (a.unit < 0) asm volatile("nanosleep.u32 0;");
 }
 
 // The lowest n bits (n may lie outside [0, 32]).
