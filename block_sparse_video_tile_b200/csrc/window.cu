@@ -145,13 +145,37 @@ static int launch_any(const WinArgs& a, const WinPlan& p, float* part, cudaStrea
   return p.step ? launch_step<D, F16>(a, p.splits, part, st) : launch_fwd<D, F16>(a, p.splits, part, st);
 }
 
-static size_t win_bwd_bytes(const vsa_window* w) {
+// Key blocks are shared among CTAs when one would walk much longer than an
+// SM's share of all the walks (kWbShares shares an SM), but no CTA walks fewer
+// than about kWbLeast blocks for it (setting one up costs as much as walking
+// several).  Walks are bounded from above: the lengths are on the device.
+constexpr int kWbShares = 2, kWbLeast = 12, kWbMost = 32;
+
+static DkvSplit dkv_split(const WinArgs& a) {
+  DkvSplit s;
+  s.blocks = (a.Nk + kWbRows - 1) / kWbRows;
+  s.heavy = static_cast<int>(std::min<long long>(s.blocks, (a.sink_tok + kWbRows - 1) / kWbRows));
+  const long long all = (a.Nq + kWbRows - 1) / kWbRows;
+  const long long seen = std::min(all, (std::min(1ll * a.window * a.unit, 1ll << 32) + a.unit + kWbRows) / kWbRows + 1);
+  const long long wh = all * a.group, wn = seen * a.group;             // blocks that a key block is walked with
+  const long long sum = (s.heavy * wh + (s.blocks - s.heavy) * wn) * a.B * a.Hkv;
+  const long long share = std::max<long long>(kWbLeast, (sum + 148 * kWbShares - 1) / (148 * kWbShares));
+  s.sh = static_cast<int>(std::min<long long>(kWbMost, std::max(1ll, (wh + share - 1) / share)));
+  s.sn = static_cast<int>(std::min<long long>(kWbMost, std::max(1ll, (wn + share - 1) / share)));
+  return s;
+}
+
+// delta, then the partial tiles of shared key blocks
+static size_t win_delta_bytes(const vsa_window* w) {
   return (static_cast<size_t>(w->B) * w->Hq * w->Nq * sizeof(float) + 255) & ~static_cast<size_t>(255);
+}
+static size_t win_bwd_bytes(const vsa_window* w, const DkvSplit& s) {
+  return win_delta_bytes(w) + static_cast<size_t>(w->B) * w->Hkv * s.tiles() * (2 * 128 * sizeof(float)) * w->d;
 }
 
 // dQ (which also writes delta), then dK and dV.
 template <int D, bool F16>
-static int launch_bwd(const WinArgs& a, cudaStream_t st) {
+static int launch_bwd(const WinArgs& a, const DkvSplit& ds, float* part, cudaStream_t st) {
   CUtensorMap mq, mg, mk, mv, mdq, mdk, mdv;
   int rc;
   if ((rc = encode_heads(&mq, a.q, a.B, a.Nq, a.Hq, D, a.qs, kWbRows, F16)) != VSA_OK ||
@@ -168,8 +192,12 @@ static int launch_bwd(const WinArgs& a, cudaStream_t st) {
     return VSA_ERR_CUDA;
   window_dq_kernel<D, F16><<<dim3((a.Nq + kWbRows - 1) / kWbRows, a.Hq, a.B), kWbThreads, smem, st>>>(mq, mg, mk, mv, mdq, a);
   if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
-  window_dkv_kernel<D, F16><<<dim3((a.Nk + kWbRows - 1) / kWbRows, a.Hkv, a.B), kWbThreads, smem, st>>>(mq, mg, mk, mv, mdk,
-                                                                                                      mdv, a);
+  window_dkv_kernel<D, F16><<<dim3(ds.ctas(), a.Hkv, a.B), kWbThreads, smem, st>>>(mq, mg, mk, mv, mdk, mdv, a, ds, part);
+  if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
+  if (ds.tiles() > 0) {
+    const int shared = ds.sn > 1 ? ds.blocks - (ds.sh > 1 ? 0 : ds.heavy) : ds.heavy;
+    window_dkv_sum_kernel<D, F16><<<dim3(shared * (D / 4), a.Hkv, a.B), 256, 0, st>>>(a, ds, part);
+  }
   return cudaGetLastError() == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
 }
 
@@ -214,7 +242,7 @@ int vsa_window_attn(const vsa_window* w, const void* q, const void* k, const voi
 size_t vsa_window_attn_bwd_workspace_bytes(const vsa_window* w) {
   WinArgs a;
   if (win_args(w, 1.f, &a) != VSA_OK || win_bwd_strides(w, &a) != VSA_OK) return 0;
-  return win_bwd_bytes(w);
+  return win_bwd_bytes(w, dkv_split(a));
 }
 
 int vsa_window_attn_bwd(const vsa_window* w, const void* d_o, const void* q, const void* k, const void* v,
@@ -230,7 +258,8 @@ int vsa_window_attn_bwd(const vsa_window* w, const void* d_o, const void* q, con
   for (const void* p : ptrs)
     if (!aligned_to(p, 16)) return VSA_ERR_ALIGNMENT;
   if (!aligned_to(lse, 4) || !aligned_to(workspace, 16)) return VSA_ERR_ALIGNMENT;
-  if (workspace == nullptr || workspace_bytes < win_bwd_bytes(w)) return VSA_ERR_WORKSPACE;
+  const DkvSplit ds = dkv_split(a);
+  if (workspace == nullptr || workspace_bytes < win_bwd_bytes(w, ds)) return VSA_ERR_WORKSPACE;
   if ((rc = check_arch()) != VSA_OK) return rc;
   if ((a.err = device_error_ptr()) == nullptr) return VSA_ERR_CUDA;
   a.q = static_cast<const uint16_t*>(q);
@@ -243,10 +272,11 @@ int vsa_window_attn_bwd(const vsa_window* w, const void* d_o, const void* q, con
   a.dk = static_cast<uint16_t*>(dk);
   a.dv = static_cast<uint16_t*>(dv);
   a.delta = static_cast<float*>(workspace);
+  float* part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + win_delta_bytes(w));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool f16 = w->dtype == VSA_DTYPE_F16;
-  if (w->d == 128) return f16 ? launch_bwd<128, true>(a, st) : launch_bwd<128, false>(a, st);
-  return f16 ? launch_bwd<64, true>(a, st) : launch_bwd<64, false>(a, st);
+  if (w->d == 128) return f16 ? launch_bwd<128, true>(a, ds, part, st) : launch_bwd<128, false>(a, ds, part, st);
+  return f16 ? launch_bwd<64, true>(a, ds, part, st) : launch_bwd<64, false>(a, ds, part, st);
 }
 
 }  // extern "C"

@@ -41,12 +41,40 @@ struct WbSmem {
   static constexpr int kASt = 3, kBSt = 2;             // stages of the walked tiles
   static constexpr int kA = 2 * kBuf, kB = kA + kASt * kBuf;
   static constexpr int kBar = kB + kBSt * kBuf;
-  static constexpr int kNumBars = 32;
+  static constexpr int kNumBars = 24;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kXch = kMisc + 16;              // dq: float [128], delta between the warpgroups
-  // dkv: (-lse * log2 e, -delta) of the walked queries, float [2 stages][2][128], in place of the third A stage
-  static constexpr int kStats = kA + 2 * kBuf;
-  static constexpr int kTotal = kXch + 512 + 1024;     // 1024: alignment of the base
+  static constexpr int kStats = kXch;                  // dkv: (-lse * log2 e, -delta) of the walked queries,
+                                                       // float [2 stages][2][128]
+  static constexpr int kEnd = kStats + 2048;
+  // what is left of a CTA's 227 KB, at most 1 KB, aligns the base
+  static constexpr int kTotal = kEnd + 1024 < 232448 ? kEnd + 1024 : 232448;
+  static_assert(kEnd + 256 <= 232448, "shared memory a CTA can have");
+};
+
+// The 1024-byte-aligned base of the buffers.  Dynamic shared memory begins on
+// such a boundary; should it not, and the buffers not fit behind the next, the
+// kernel reports it and does nothing.
+template <int D>
+__device__ __forceinline__ bool wb_base(const WinArgs& a, uint32_t raw, uint32_t& base) {
+  uint32_t size;
+  asm volatile("mov.u32 %0, %%dynamic_smem_size;" : "=r"(size));
+  base = (raw + 1023u) & ~1023u;
+  if (base - raw + WbSmem<D>::kEnd <= size) return true;
+  if (threadIdx.x == 0) atomicCAS(a.err, 0u, 1u);
+  return false;
+}
+
+// How the queries that see a key block are shared out: the first `heavy` key
+// blocks (they hold first units, which every later query sees) among sh CTAs
+// each, the others among sn.  A block with several CTAs gets its sums as float32
+// partial tiles, [dK, dV][128 rows][D] a CTA, added in order by
+// window_dkv_sum_kernel.
+struct DkvSplit {
+  int blocks, heavy, sh, sn;
+  __host__ __device__ int ctas() const { return heavy * sh + (blocks - heavy) * sn; }
+  // partial tiles of one (batch, key/value head)
+  __host__ __device__ int tiles() const { return (sh > 1 ? heavy * sh : 0) + (sn > 1 ? (blocks - heavy) * sn : 0); }
 };
 
 // Stages an O-shaped tile of this thread's row (128 columns of TMEM at t, D of
@@ -97,9 +125,10 @@ __global__ void __launch_bounds__(kWbThreads, 1)
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ CUtensorMap tmDQ, const __grid_constant__ WinArgs a) {
   using L = WbSmem<D>;
-  extern __shared__ unsigned char smem_raw[];
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint32_t base;
+  if (!wb_base<D>(a, raw, base)) return;
   unsigned char* sp = smem_raw + (base - raw);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sp + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + L::kMisc + 4);
@@ -352,7 +381,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
 // ------------------------------------------------------------------ dK, dV
 enum : int {
   DK_OWN = 0, DK_S = 1, DK_P = 2 /* [half] */, DK_DP = 4, DK_DS = 5, DK_OUT = 6 /* [2] */, DK_DRAIN = 8,
-  DK_Q_FULL = 9 /* [2] */, DK_Q_EMPTY = 11, DK_G_FULL = 13, DK_G_EMPTY = 15, DK_ST_FULL = 17, DK_ST_EMPTY = 19
+  DK_Q_FULL = 9 /* [3] */, DK_Q_EMPTY = 12, DK_G_FULL = 15 /* [2] */, DK_G_EMPTY = 17, DK_ST_FULL = 19, DK_ST_EMPTY = 21
 };
 
 // The CTA's 128 keys are the rows, the queries of a block the columns.  TMEM:
@@ -367,11 +396,12 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
                       const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmDK, const __grid_constant__ CUtensorMap tmDV,
-                      const __grid_constant__ WinArgs a) {
+                      const __grid_constant__ WinArgs a, const DkvSplit ds, float* part) {
   using L = WbSmem<D>;
-  extern __shared__ unsigned char smem_raw[];
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint32_t base;
+  if (!wb_base<D>(a, raw, base)) return;
   unsigned char* sp = smem_raw + (base - raw);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sp + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + L::kMisc + 4);
@@ -380,7 +410,12 @@ __global__ void __launch_bounds__(kWbThreads, 1)
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int hk = blockIdx.y, b = blockIdx.z;
-  const int c0 = blockIdx.x * kWbRows;                 // first keys first: they may be seen by every query
+  // first keys first: they may be seen by every query
+  const int x = blockIdx.x - ds.heavy * ds.sh;
+  const bool hv = x < 0;
+  const int S = hv ? ds.sh : ds.sn;                    // CTAs of this key block
+  const int blk = hv ? blockIdx.x / S : ds.heavy + x / S, sp_i = hv ? blockIdx.x % S : x % S;
+  const int c0 = blk * kWbRows;
   const int len = win_len(a, b), start = win_start(a, b, len);
   // queries that see some key of [c0, c1): one range of rows, [qlo, qhi)
   int qb0 = 0, nq = 0;
@@ -394,13 +429,15 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       nq = static_cast<int>((qhi + kWbRows - 1) / kWbRows) - qb0;
     }
   }
-  const int n = nq * a.group;
+  const int n_all = nq * a.group;
+  const int j0 = static_cast<int>(static_cast<long long>(n_all) * sp_i / S);
+  const int n = static_cast<int>(static_cast<long long>(n_all) * (sp_i + 1) / S) - j0;   // this CTA's walk
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
       uint32_t cnt = 1;
       if (i == DK_P || i == DK_P + 1 || i == DK_DS || i == DK_ST_EMPTY || i == DK_ST_EMPTY + 1) cnt = 256;
-      if (i == DK_DRAIN || (i >= DK_Q_EMPTY && i < DK_Q_EMPTY + 2) || (i >= DK_G_EMPTY && i < DK_G_EMPTY + 2)) cnt = 2;
+      if (i == DK_DRAIN || (i >= DK_Q_EMPTY && i < DK_Q_EMPTY + 3) || (i >= DK_G_EMPTY && i < DK_G_EMPTY + 2)) cnt = 2;
       if (i == DK_ST_FULL || i == DK_ST_FULL + 1) cnt = 32;
       mbar_init(bar(i), cnt);
     }
@@ -416,7 +453,8 @@ __global__ void __launch_bounds__(kWbThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t tS = tmem, tDP = tmem + 128, tDV = tmem + 256, tDK = tmem + 384;
-  // walked block j: query head hk * group + j / nq, rows from (qb0 + j % nq) * 128
+  // walked block j: query head hk * group + (j0 + j) / nq, rows from (qb0 + (j0 + j) % nq) * 128
+  const int h_first = hk * a.group + (nq > 0 ? j0 / nq : 0), q_first = nq > 0 ? j0 % nq : 0;
 
   if (warp == 8) {
     // ====================================================== TMA producer
@@ -426,14 +464,14 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         tma_load_4d(base + L::kOwn0 + sl * L::kSlab, &tmK, bar(DK_OWN), sl * 64, c0, hk, b);
         tma_load_4d(base + L::kOwn1 + sl * L::kSlab, &tmV, bar(DK_OWN), sl * 64, c0, hk, b);
       }
-      int qd = 0, gd = 0, h = hk * a.group, qi = 0;
+      int qd = 0, gd = 0, h = h_first, qi = q_first;
       for (int j = 0; j < n; ++j) {
-        const int st = j & 1, i0 = (qb0 + qi) * kWbRows;
-        if (j >= 2 && !mbar_wait(bar(DK_Q_EMPTY + st), ((j >> 1) - 1) & 1, abort_flag, a.err)) break;
+        const int st = j & 1, qs = j % L::kASt, i0 = (qb0 + qi) * kWbRows;
+        if (j >= L::kASt && !mbar_wait(bar(DK_Q_EMPTY + qs), (j / L::kASt - 1) & 1, abort_flag, a.err)) break;
         qd = j + 1;
-        mbar_arrive_expect_tx(bar(DK_Q_FULL + st), L::kBuf);
+        mbar_arrive_expect_tx(bar(DK_Q_FULL + qs), L::kBuf);
         for (int sl = 0; sl < L::kSlabs; ++sl)
-          tma_load_4d(base + L::kA + st * L::kBuf + sl * L::kSlab, &tmQ, bar(DK_Q_FULL + st), sl * 64, i0, h, b);
+          tma_load_4d(base + L::kA + qs * L::kBuf + sl * L::kSlab, &tmQ, bar(DK_Q_FULL + qs), sl * 64, i0, h, b);
         if (j >= 2 && !mbar_wait(bar(DK_G_EMPTY + st), ((j >> 1) - 1) & 1, abort_flag, a.err)) break;
         gd = j + 1;
         mbar_arrive_expect_tx(bar(DK_G_FULL + st), L::kBuf);
@@ -441,14 +479,15 @@ __global__ void __launch_bounds__(kWbThreads, 1)
           tma_load_4d(base + L::kB + st * L::kBuf + sl * L::kSlab, &tmG, bar(DK_G_FULL + st), sl * 64, i0, h, b);
         if (++qi == nq) { qi = 0; ++h; }
       }
-      for (int j = max(0, qd - 2); j < qd; ++j) mbar_wait(bar(DK_Q_FULL + (j & 1)), (j >> 1) & 1, nullptr, a.err);
+      for (int j = max(0, qd - L::kASt); j < qd; ++j)
+        mbar_wait(bar(DK_Q_FULL + j % L::kASt), (j / L::kASt) & 1, nullptr, a.err);
       for (int j = max(0, gd - 2); j < gd; ++j) mbar_wait(bar(DK_G_FULL + (j & 1)), (j >> 1) & 1, nullptr, a.err);
       mbar_wait(bar(DK_OWN), 0, nullptr, a.err);
     }
     __syncwarp();
   } else if (warp == 9) {
     // ====================================================== LSE and delta
-    int h = hk * a.group, qi = 0;
+    int h = h_first, qi = q_first;
     for (int j = 0; j < n; ++j) {
       const int st = j & 1, i0 = (qb0 + qi) * kWbRows;
       const size_t row0 = (static_cast<size_t>(b) * a.Hq + h) * a.Nq;
@@ -476,36 +515,44 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     constexpr uint32_t idO = idesc_f16kind_f32(128, D, true, F16);
     const bool first = warp == 10;                     // S, dV; else dP, dK
     bool ok = n == 0 || __all_sync(0xffffffffu, mbar_wait(bar(DK_OWN), 0, abort_flag, a.err));
-    // S(j) = K Q(j)^T, or dP(j) = V dO(j)^T
-    auto make = [&](int j) {
-      const int st = j & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar((first ? DK_Q_FULL : DK_G_FULL) + st), (j >> 1) & 1, abort_flag, a.err));
-      if (!ok) return;
-      tc_fence_after();
-      if (elect_one_sync()) {
-        const uint32_t own = base + (first ? L::kOwn0 : L::kOwn1);
-        const uint32_t in = base + (first ? L::kA : L::kB) + st * L::kBuf;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const int off = (kk / 4) * L::kSlab + (kk % 4) * 32;
-          mma_ss(first ? tS : tDP, smem_desc_sw128(own + off, 16, 1024), smem_desc_sw128(in + off, 16, 1024), idS,
-                 kk > 0 ? 1u : 0u);
-        }
-        mma_commit(bar(first ? DK_S : DK_DP));
-        mma_commit(bar((first ? DK_Q_EMPTY : DK_G_EMPTY) + st));
-      }
-      __syncwarp();
+    auto wait_in = [&](int j, bool g) {                // Q(j) or dO(j) has landed
+      ok = __all_sync(0xffffffffu, g ? mbar_wait(bar(DK_G_FULL + (j & 1)), (j >> 1) & 1, abort_flag, a.err)
+                                     : mbar_wait(bar(DK_Q_FULL + j % L::kASt), (j / L::kASt) & 1, abort_flag, a.err));
     };
-    if (ok && n > 0) make(0);
+    // (elected lane) S(j) = K Q(j)^T, or dP(j) = V dO(j)^T
+    auto make = [&](int j) {
+      const uint32_t own = base + (first ? L::kOwn0 : L::kOwn1);
+      const uint32_t in = base + (first ? L::kA + (j % L::kASt) * L::kBuf : L::kB + (j & 1) * L::kBuf);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const int off = (kk / 4) * L::kSlab + (kk % 4) * 32;
+        mma_ss(first ? tS : tDP, smem_desc_sw128(own + off, 16, 1024), smem_desc_sw128(in + off, 16, 1024), idS,
+               kk > 0 ? 1u : 0u);
+      }
+      mma_commit(bar(first ? DK_S : DK_DP));
+      mma_commit(bar(first ? DK_Q_EMPTY + j % L::kASt : DK_G_EMPTY + (j & 1)));
+    };
+    if (ok && n > 0) {
+      wait_in(0, !first);
+      if (ok) {
+        tc_fence_after();
+        if (elect_one_sync()) make(0);
+        __syncwarp();
+      }
+    }
     for (int j = 0; j < n && ok; ++j) {
+      // The next block's scores are queued right behind this block's product:
+      // their operand is waited for before it, since a barrier test behind
+      // queued MMAs waits for them to drain -- and then the other warp's MMAs
+      // would come between (dK and dP before S: 3300 clk a block).
       const int st = j & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar((first ? DK_G_FULL : DK_Q_FULL) + st), (j >> 1) & 1, abort_flag, a.err));
-      if (!ok) break;
+      wait_in(j, first);
       if (first) {
         const uint32_t gb = base + L::kB + st * L::kBuf;
 #pragma unroll
         for (int hf = 0; hf < 2 && ok; ++hf) {
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(DK_P + hf), j & 1, abort_flag, a.err));
+          if (hf == 1 && j + 1 < n) wait_in(j + 1, false);
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(DK_P + hf), j & 1, abort_flag, a.err));
           if (!ok) break;
           tc_fence_after();
           if (elect_one_sync()) {
@@ -516,6 +563,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
                      (j > 0 || hf > 0 || e > 0) ? 1u : 0u);
             }
             if (hf == 1) {
+              if (j + 1 < n) make(j + 1);
               mma_commit(bar(DK_G_EMPTY + st));
               if (j == n - 1) mma_commit(bar(DK_OUT));
             }
@@ -523,21 +571,22 @@ __global__ void __launch_bounds__(kWbThreads, 1)
           __syncwarp();
         }
       } else {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(DK_DS), j & 1, abort_flag, a.err));
+        if (ok && j + 1 < n) wait_in(j + 1, true);
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(DK_DS), j & 1, abort_flag, a.err));
         if (!ok) break;
         tc_fence_after();
         if (elect_one_sync()) {
-          const uint32_t qb = base + L::kA + st * L::kBuf;
+          const uint32_t qb = base + L::kA + (j % L::kASt) * L::kBuf;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             mma_ts(tDK, tDP + 64u * (kk / 4) + 8u * (kk % 4), smem_desc_sw128(qb + kk * 2048, L::kSlab, 1024), idO,
                    (j > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(bar(DK_Q_EMPTY + st));
+          if (j + 1 < n) make(j + 1);
+          mma_commit(bar(DK_Q_EMPTY + j % L::kASt));
           if (j == n - 1) mma_commit(bar(DK_OUT + 1));
         }
         __syncwarp();
       }
-      if (ok && j + 1 < n) make(j + 1);
     }
     if (elect_one_sync()) mma_commit(bar(DK_DRAIN));
     __syncwarp();
@@ -559,7 +608,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     }
     bool ok = true;
     const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2);
-    int qi = 0;
+    int qi = q_first;
     for (int j = 0; j < n; ++j) {
       const int st = j & 1, i0 = (qb0 + qi) * kWbRows;
       if (++qi == nq) qi = 0;
@@ -570,14 +619,14 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       const int il = min(i0 + kWbRows, a.Nq) - 1;
       if (start + i0 < 0 || (masked && row_vis(a, len, start + il).hi == row_vis(a, len, start + il).lo &&
                              row_vis(a, len, start + il).first == 0)) {
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(DK_Q_FULL + st), (j >> 1) & 1, abort_flag, a.err) &&
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(DK_Q_FULL + j % L::kASt), (j / L::kASt) & 1, abort_flag, a.err) &&
                                          mbar_wait(bar(DK_G_FULL + st), (j >> 1) & 1, abort_flag, a.err))) {
           ok = false;
           break;
         }
         const RowVis v = row_vis(a, len, start + i0 + r);
         if (v.hi == v.lo && v.first == 0 && i0 + r < a.Nq)
-          zero_row<D>(base + (w == 0 ? L::kA : L::kB) + st * L::kBuf, r);
+          zero_row<D>(base + (w == 0 ? L::kA + (j % L::kASt) * L::kBuf : L::kB + st * L::kBuf), r);
         fence_proxy_async_smem();
       }
       if (!__all_sync(0xffffffffu, mbar_wait(bar(DK_ST_FULL + st), (j >> 1) & 1, abort_flag, a.err) &&
@@ -657,7 +706,29 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       mbar_arrive(bar(DK_ST_EMPTY + st));
     }
     // ---- epilogue: warpgroup 0 writes dV through V's buffer, 1 dK through K's
-    if (n > 0) {
+    if (S > 1) {
+      if (n > 0 && ok)
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(DK_OUT), 0, abort_flag, a.err) &&
+                                         mbar_wait(bar(DK_OUT + 1), 0, abort_flag, a.err));
+      tc_fence_after();
+      const int tile = hv ? blockIdx.x : (ds.sh > 1 ? ds.heavy * ds.sh : 0) + x;
+      float* op = part + ((static_cast<size_t>(b) * a.Hkv + hk) * ds.tiles() + tile) * (2 * 128 * D) +
+                  (w == 0 ? 128 * D : 0) + r * D;
+#pragma unroll
+      for (int q4 = 0; q4 < D / 32; ++q4) {
+        uint32_t ov[32];
+        if (n > 0) {
+          tmem_ld32((w == 0 ? tDV : tDK) + lane_base + 32u * q4, ov);
+          tmem_wait_ld();
+        }
+        if (ok) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            reinterpret_cast<uint4*>(op + 32 * q4)[e] =
+                n > 0 ? make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]) : make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+    } else if (n > 0) {
       if (ok)
         ok = __all_sync(0xffffffffu, mbar_wait(bar(DK_OUT), 0, abort_flag, a.err) &&
                                          mbar_wait(bar(DK_OUT + 1), 0, abort_flag, a.err));
@@ -686,6 +757,34 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// dK and dV rows of the key blocks that several CTAs shared: their partial
+// tiles added in order.  One thread 4 channels of a row.
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) window_dkv_sum_kernel(const __grid_constant__ WinArgs a, const DkvSplit ds,
+                                                             const float* part) {
+  const int first = ds.sh > 1 ? 0 : ds.heavy;           // first shared block
+  const int blk = first + blockIdx.x / (D / 4), hk = blockIdx.y, b = blockIdx.z;     // D / 4 CTAs of 256 a block: 2 x 128 x D / 4
+  const bool hv = blk < ds.heavy;
+  const int S = hv ? ds.sh : ds.sn;
+  if (S == 1) return;
+  const int tile = hv ? blk * S : (ds.sh > 1 ? ds.heavy * ds.sh : 0) + (blk - ds.heavy) * S;
+  const int at = (blockIdx.x % (D / 4)) * 256 + threadIdx.x;                         // float4 of a tile
+  const float4* p = reinterpret_cast<const float4*>(
+                        part + ((static_cast<size_t>(b) * a.Hkv + hk) * ds.tiles() + tile) * (2 * 128 * D)) + at;
+  float4 s = p[0];
+  for (int i = 1; i < S; ++i) {
+    const float4 v = p[static_cast<size_t>(i) * (2 * 128 * D / 4)];
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+  const bool is_v = at >= 128 * D / 4;
+  const int e = is_v ? at - 128 * D / 4 : at;
+  const int key = blk * kWbRows + e / (D / 4), ch = (e % (D / 4)) * 4;
+  if (key >= a.Nk) return;
+  const float f = is_v ? 1.f : a.scale;
+  uint16_t* o = is_v ? a.dv + b * a.dvs[0] + key * a.dvs[1] + hk * a.dvs[2] : a.dk + b * a.dks[0] + key * a.dks[1] + hk * a.dks[2];
+  *reinterpret_cast<uint2*>(o + ch) = make_uint2(pack_elem2<F16>(s.x * f, s.y * f), pack_elem2<F16>(s.z * f, s.w * f));
 }
 
 }  // namespace vsa
