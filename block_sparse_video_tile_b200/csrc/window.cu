@@ -77,10 +77,16 @@ static int encode_heads(CUtensorMap* m, const void* ptr, int B, int N, int H, in
 // when its CTAs are too few, as far as the most keys that a row can see allow
 // (the lengths are on the device).
 constexpr int kWsMaxRows = 64;
+// CTAs that a step call asks for, two an SM: with splits joined in a cluster 1.5
+// rounds of them (64 row tiles of 16384 keys: 5 splits 127 us, 7 95 us, 8 94 us,
+// 18 and a second kernel 104 us; 256 tiles of 2048: 2 splits 51 us, 8 84 us), with
+// the second kernel one round (8 tiles of 65536: 51 us, two rounds 56 us).
+constexpr int kWsClusterCtas = 148 * 3, kWsSplitCtas = 148 * 2;
 
 struct WinPlan {
-  bool step;
+  bool step, cluster;        // cluster: the splits are joined by the kernel itself
   int splits;
+  int partial() const { return cluster ? 1 : splits; }      // splits that leave partial results
 };
 
 static WinPlan win_plan(const WinArgs& a) {
@@ -92,8 +98,12 @@ static WinPlan win_plan(const WinArgs& a) {
   if (p.step) {
     const long long ctas = 1ll * a.B * a.Hkv * ((rows + kWsRows - 1) / kWsRows);
     const long long most = std::max(1ll, keys / (kWsKeys * kWsWarps * 2));   // two tiles a warp at least
-    p.splits = static_cast<int>(std::max(1ll, std::min({(148 * 8 + ctas - 1) / ctas, most, 256ll})));
+    const long long want = std::min((kWsClusterCtas + ctas - 1) / ctas, most);
+    p.cluster = want <= kWsCluster;
+    p.splits = static_cast<int>(std::max(1ll, p.cluster ? want : std::min({(kWsSplitCtas + ctas - 1) / ctas, most, 256ll})));
+    if (p.splits == 1) p.cluster = false;
   } else {
+    p.cluster = false;
     p.splits = 1;
   }
   return p;
@@ -107,19 +117,29 @@ template <int D, bool F16>
 static int launch_combine(const WinArgs& a, int splits, const float* part, cudaStream_t st) {
   if (splits == 1) return VSA_OK;
   const long long rows = 1ll * a.B * a.Hq * a.Nq;
-  window_combine_kernel<D, F16><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(a, splits, part);
+  window_combine_kernel<D, F16><<<static_cast<unsigned>(rows), 256, 0, st>>>(a, splits, part);
   return cudaGetLastError() == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
 }
 
-template <int D, bool F16>
-static int launch_step(const WinArgs& a, int splits, float* part, cudaStream_t st) {
+template <int D, bool F16, bool CLUSTER>
+static int launch_step_as(const WinArgs& a, int splits, float* part, cudaStream_t st) {
   constexpr int smem = WsSmem<D>::kTotal;
-  if (cudaFuncSetAttribute(window_step_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  if (cudaFuncSetAttribute(window_step_kernel<D, F16, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+      cudaSuccess)
     return VSA_ERR_CUDA;
-  const int tiles = (a.Nq * a.group + kWsRows - 1) / kWsRows;
-  window_step_kernel<D, F16><<<dim3(splits, a.Hkv * tiles, a.B), kWsThreads, smem, st>>>(a, splits, part);
-  if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
-  return launch_combine<D, F16>(a, splits, part, st);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(splits, a.Hkv * ((a.Nq * a.group + kWsRows - 1) / kWsRows), a.B);
+  cfg.blockDim = dim3(kWsThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = CLUSTER ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, window_step_kernel<D, F16, CLUSTER>, a, splits, part) != cudaSuccess) return VSA_ERR_CUDA;
+  return CLUSTER ? VSA_OK : launch_combine<D, F16>(a, splits, part, st);
 }
 
 template <int D, bool F16>
@@ -142,7 +162,8 @@ static int launch_fwd(const WinArgs& a, int splits, float* part, cudaStream_t st
 
 template <int D, bool F16>
 static int launch_any(const WinArgs& a, const WinPlan& p, float* part, cudaStream_t st) {
-  return p.step ? launch_step<D, F16>(a, p.splits, part, st) : launch_fwd<D, F16>(a, p.splits, part, st);
+  if (!p.step) return launch_fwd<D, F16>(a, p.splits, part, st);
+  return p.cluster ? launch_step_as<D, F16, true>(a, p.splits, part, st) : launch_step_as<D, F16, false>(a, p.splits, part, st);
 }
 
 // Key blocks are shared among CTAs when one would walk much longer than an
@@ -210,7 +231,7 @@ extern "C" {
 size_t vsa_window_attn_workspace_bytes(const vsa_window* w) {
   WinArgs a;
   if (win_args(w, 1.f, &a) != VSA_OK) return 0;
-  return win_fwd_bytes(a, w->d, win_plan(a).splits);
+  return win_fwd_bytes(a, w->d, win_plan(a).partial());
 }
 
 int vsa_window_attn(const vsa_window* w, const void* q, const void* k, const void* v, float softmax_scale, void* o,
@@ -223,7 +244,7 @@ int vsa_window_attn(const vsa_window* w, const void* q, const void* k, const voi
       !aligned_to(workspace, 16))
     return VSA_ERR_ALIGNMENT;
   const WinPlan plan = win_plan(a);
-  const size_t need = win_fwd_bytes(a, w->d, plan.splits);
+  const size_t need = win_fwd_bytes(a, w->d, plan.partial());
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return VSA_ERR_WORKSPACE;
   if ((rc = check_arch()) != VSA_OK) return rc;
   if ((a.err = device_error_ptr()) == nullptr) return VSA_ERR_CUDA;

@@ -495,13 +495,16 @@ __global__ void __launch_bounds__(kWfThreads, 1)
 }
 
 // O = sum_s e^(lse_s - L) O_s, L = log sum_s e^lse_s over the splits of a row:
-// one warp a row, D / 32 channels a lane; reads what the splits wrote once.
+// a CTA a row, its eight warps every eighth split (there are few rows here, and
+// up to hundreds of splits), D / 32 channels a lane; reads what the splits
+// wrote once.
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) window_combine_kernel(const __grid_constant__ WinArgs a, int splits, const float* part) {
-  const size_t rows = static_cast<size_t>(a.B) * a.Hq * a.Nq;
-  const size_t row = static_cast<size_t>(blockIdx.x) * 8 + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  if (row >= rows) return;
+  constexpr int W = 8;
+  __shared__ float so[W][D];
+  __shared__ float sw[W];
+  const size_t rows = static_cast<size_t>(a.B) * a.Hq * a.Nq, row = blockIdx.x;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const float* ls = part + splits * rows * D + row;
   float mx = -INFINITY;
   for (int s = lane; s < splits; s += 32) mx = fmaxf(mx, ls[s * rows]);
@@ -509,22 +512,35 @@ __global__ void __launch_bounds__(256) window_combine_kernel(const __grid_consta
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   float acc[D / 32] = {}, sum = 0.f;
   if (mx != -INFINITY) {
-    for (int s = 0; s < splits; ++s) {
+#pragma unroll 4
+    for (int s = warp; s < splits; s += W) {
       const float w = exp2f((ls[s * rows] - mx) * 1.4426950408889634f);
       sum += w;
-      const float* op = part + (s * rows + row) * D + lane * (D / 32);
+      const float* op = part + (s * rows + row) * D + lane;
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(w, op[e], acc[e]);
+      for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(w, op[32 * e], acc[e]);
     }
+  }
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) so[warp][lane + 32 * e] = acc[e];
+  if (lane == 0) sw[warp] = sum;
+  __syncthreads();
+  if (threadIdx.x >= D / 2) return;
+  sum = 0.f;
+  float x = 0.f, y = 0.f;
+#pragma unroll
+  for (int k = 0; k < W; ++k) {
+    sum += sw[k];
+    x += so[k][2 * threadIdx.x];
+    y += so[k][2 * threadIdx.x + 1];
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   const int i = static_cast<int>(row % a.Nq);
   const size_t bh = row / a.Nq;
   const int h = static_cast<int>(bh % a.Hq), b = static_cast<int>(bh / a.Hq);
-  uint32_t* o = reinterpret_cast<uint32_t*>(a.out + b * a.os[0] + i * a.os[1] + h * a.os[2]) + lane * (D / 64);
-#pragma unroll
-  for (int e = 0; e < D / 64; ++e) o[e] = pack_elem2<F16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  if (lane == 0) a.lse[row] = sum > 0.f ? mx + logf(sum) : -INFINITY;
+  reinterpret_cast<uint32_t*>(a.out + b * a.os[0] + i * a.os[1] + h * a.os[2])[threadIdx.x] =
+      pack_elem2<F16>(x * inv, y * inv);
+  if (threadIdx.x == 0) a.lse[row] = sum > 0.f ? mx + logf(sum) : -INFINITY;
 }
 
 }  // namespace vsa

@@ -10,8 +10,10 @@
 // 16-key tiles, their four warps every fourth tile of the run.  A warp keeps
 // its own running maximum, sum and O and its own ring of kWsStages tiles
 // filled by cp.async (8 KB of K and V a tile at d = 128), so no warp waits for
-// another before the end, where the four are joined through shared memory and
-// the splits by window_combine_kernel.
+// another before the end, where the four are joined through shared memory.  Up
+// to kWsCluster splits are a cluster, whose CTAs then join their results through
+// distributed shared memory (no second launch: window_step_small 9.0 us of two
+// kernels); more go through window_combine_kernel.
 #pragma once
 
 #include "window_args.cuh"
@@ -24,14 +26,40 @@ constexpr int kWsWarps = 4, kWsThreads = 32 * kWsWarps;
 constexpr int kWsKeys = 16;              // keys a tile
 constexpr int kWsRows = 16;              // query rows a CTA (token-major, then head of the group)
 constexpr int kWsStages = 3;
+constexpr int kWsCluster = 8;            // splits that are joined as one cluster
 
 template <int D>
 struct WsSmem {
   static constexpr int kTile = 2 * kWsKeys * D * 2;              // K, then V
   static constexpr int kRing = kWsWarps * kWsStages * kTile;
   static constexpr int kJoin = kWsWarps * kWsRows * (D + 2) * 4;  // O, m, l of each warp (over the ring)
-  static constexpr int kTotal = kRing > kJoin ? kRing : kJoin;
+  static constexpr int kRes = (kJoin + 127) & ~127;               // the CTA's O, m, l for its cluster
+  static constexpr int kEnd = kRes + kWsRows * (D + 2) * 4;
+  static constexpr int kTotal = kRing > kEnd ? kRing : kEnd;
 };
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of a shared-memory location in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -59,9 +87,10 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// grid (splits, Hkv * row tiles, B).  splits == 1 writes O and LSE, else the
-// partial results of window_fwd_kernel's splits.
-template <int D, bool F16>
+// grid (splits, Hkv * row tiles, B); CLUSTER: the splits of a row tile are one
+// cluster.  That and splits == 1 write O and LSE, else the partial results of
+// window_fwd_kernel's splits.
+template <int D, bool F16, bool CLUSTER>
 __global__ void __launch_bounds__(kWsThreads) window_step_kernel(const __grid_constant__ WinArgs a, int splits, float* part) {
   using L = WsSmem<D>;
   constexpr int CH = D / 8;                                       // 16-byte chunks of a row
@@ -223,40 +252,88 @@ __global__ void __launch_bounds__(kWsThreads) window_step_kernel(const __grid_co
   }
   __syncthreads();
   constexpr int TPR = kWsThreads / kWsRows;                       // threads a row
+  constexpr int CPT = D / TPR / 4;                                // float4 a thread
   const int rr = threadIdx.x / TPR, part_c = threadIdx.x % TPR, r = r0 + rr;
-  if (r >= R) return;
-  float mt = -INFINITY, lt = 0.f, w[kWsWarps];
+  float mt = -INFINITY, lt = 0.f;
+  float4 acc[CPT];
+  {
+    float w[kWsWarps];
 #pragma unroll
-  for (int k = 0; k < kWsWarps; ++k) mt = fmaxf(mt, jm[(k * kWsRows + rr) * 2]);
+    for (int k = 0; k < kWsWarps; ++k) mt = fmaxf(mt, jm[(k * kWsRows + rr) * 2]);
 #pragma unroll
-  for (int k = 0; k < kWsWarps; ++k) {
-    w[k] = mt == -INFINITY ? 0.f : ex2_approx(jm[(k * kWsRows + rr) * 2] - mt);
-    lt = fmaf(w[k], jm[(k * kWsRows + rr) * 2 + 1], lt);
+    for (int k = 0; k < kWsWarps; ++k) {
+      w[k] = mt == -INFINITY ? 0.f : ex2_approx(jm[(k * kWsRows + rr) * 2] - mt);
+      lt = fmaf(w[k], jm[(k * kWsRows + rr) * 2 + 1], lt);
+    }
+#pragma unroll
+    for (int e = 0; e < CPT; ++e) {
+      acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kWsWarps; ++k) {
+        const float4 x = *reinterpret_cast<const float4*>(jo + (k * kWsRows + rr) * D + 4 * (part_c + TPR * e));
+        acc[e].x = fmaf(w[k], x.x, acc[e].x);
+        acc[e].y = fmaf(w[k], x.y, acc[e].y);
+        acc[e].z = fmaf(w[k], x.z, acc[e].z);
+        acc[e].w = fmaf(w[k], x.w, acc[e].w);
+      }
+    }
   }
+  bool write = r < R;
+  if (CLUSTER) {
+    // every CTA shows its rows; row rr is joined and written by CTA rr % splits
+    float* res = reinterpret_cast<float*>(smem + L::kRes);        // [row][D], then [row][2]
+#pragma unroll
+    for (int e = 0; e < CPT; ++e) *reinterpret_cast<float4*>(res + rr * D + 4 * (part_c + TPR * e)) = acc[e];
+    if (part_c == 0) *reinterpret_cast<float2*>(res + kWsRows * D + 2 * rr) = make_float2(mt, lt);
+    cluster_sync();
+    write = write && rr % splits == split;
+    if (write) {
+      const uint32_t mine = smem_u32(res);
+      float ms[kWsCluster], mx = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kWsCluster; ++k) {
+        ms[k] = -INFINITY;
+        if (k < splits) ms[k] = ld_cluster2(cluster_addr(mine + (kWsRows * D + 2 * rr) * 4, k)).x;
+        mx = fmaxf(mx, ms[k]);
+      }
+      mt = mx;
+      lt = 0.f;
+#pragma unroll
+      for (int e = 0; e < CPT; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kWsCluster; ++k) {
+        if (k >= splits) break;
+        const float w = mx == -INFINITY ? 0.f : ex2_approx(ms[k] - mx);
+        lt = fmaf(w, ld_cluster2(cluster_addr(mine + (kWsRows * D + 2 * rr) * 4, k)).y, lt);
+#pragma unroll
+        for (int e = 0; e < CPT; ++e) {
+          const float4 x = ld_cluster4(cluster_addr(mine + (rr * D + 4 * (part_c + TPR * e)) * 4, k));
+          acc[e].x = fmaf(w, x.x, acc[e].x);
+          acc[e].y = fmaf(w, x.y, acc[e].y);
+          acc[e].z = fmaf(w, x.z, acc[e].z);
+          acc[e].w = fmaf(w, x.w, acc[e].w);
+        }
+      }
+    }
+    cluster_sync();                                               // nobody leaves while its rows are read
+  }
+  if (!write) return;
   const float inv = lt > 0.f ? 1.f / lt : 0.f;
   const float lse = lt > 0.f ? (mt + log2f(lt)) * 0.69314718055994530942f : -INFINITY;
   const int i = r / a.group, h = hk * a.group + r % a.group;
   const size_t row = (static_cast<size_t>(b) * a.Hq + h) * a.Nq + i, rows = static_cast<size_t>(a.B) * a.Hq * a.Nq;
+  const bool partial = !CLUSTER && splits > 1;
   uint16_t* out = a.out + b * a.os[0] + i * a.os[1] + h * a.os[2];
-  float* po = splits > 1 ? part + (split * rows + row) * D : nullptr;
+  float* po = partial ? part + (split * rows + row) * D : nullptr;
 #pragma unroll
-  for (int e = 0; e < D / TPR / 4; ++e) {
+  for (int e = 0; e < CPT; ++e) {
     const int ch = 4 * (part_c + TPR * e);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < kWsWarps; ++k) {
-      const float4 x = *reinterpret_cast<const float4*>(jo + (k * kWsRows + rr) * D + ch);
-      acc.x = fmaf(w[k], x.x, acc.x);
-      acc.y = fmaf(w[k], x.y, acc.y);
-      acc.z = fmaf(w[k], x.z, acc.z);
-      acc.w = fmaf(w[k], x.w, acc.w);
-    }
-    acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
-    if (splits > 1) *reinterpret_cast<float4*>(po + ch) = acc;
-    else *reinterpret_cast<uint2*>(out + ch) = make_uint2(pack_elem2<F16>(acc.x, acc.y), pack_elem2<F16>(acc.z, acc.w));
+    const float4 x = make_float4(acc[e].x * inv, acc[e].y * inv, acc[e].z * inv, acc[e].w * inv);
+    if (partial) *reinterpret_cast<float4*>(po + ch) = x;
+    else *reinterpret_cast<uint2*>(out + ch) = make_uint2(pack_elem2<F16>(x.x, x.y), pack_elem2<F16>(x.z, x.w));
   }
   if (part_c == 0) {
-    if (splits > 1) part[splits * rows * D + split * rows + row] = lse;
+    if (partial) part[splits * rows * D + split * rows + row] = lse;
     else a.lse[row] = lse;
   }
 }
