@@ -209,11 +209,18 @@ static int launch_bwd(const WinArgs& a, const DkvSplit& ds, float* part, cudaStr
     return rc;
   constexpr int smem = WbSmem<D>::kTotal;
   if (cudaFuncSetAttribute(window_dq_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-      cudaFuncSetAttribute(window_dkv_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      cudaFuncSetAttribute(window_dkv_kernel<D, F16, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+          cudaSuccess ||
+      cudaFuncSetAttribute(window_dkv_kernel<D, F16, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+          cudaSuccess)
     return VSA_ERR_CUDA;
   window_dq_kernel<D, F16><<<dim3((a.Nq + kWbRows - 1) / kWbRows, a.Hq, a.B), kWbThreads, smem, st>>>(mq, mg, mk, mv, mdq, a);
   if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
-  window_dkv_kernel<D, F16><<<dim3(ds.ctas(), a.Hkv, a.B), kWbThreads, smem, st>>>(mq, mg, mk, mv, mdk, mdv, a, ds, part);
+  const dim3 grid(ds.ctas(), a.Hkv, a.B);
+  if (ds.tiles() > 0)
+    window_dkv_kernel<D, F16, true><<<grid, kWbThreads, smem, st>>>(mq, mg, mk, mv, mdk, mdv, a, ds, part);
+  else
+    window_dkv_kernel<D, F16, false><<<grid, kWbThreads, smem, st>>>(mq, mg, mk, mv, mdk, mdv, a, ds, part);
   if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
   if (ds.tiles() > 0) {
     const int shared = ds.sn > 1 ? ds.blocks - (ds.sh > 1 ? 0 : ds.heavy) : ds.heavy;

@@ -118,7 +118,9 @@ enum : int {
 // TMEM: two score buffers (dS of a warpgroup's 64 keys over the first 32
 // columns of its half), dP, dQ.  Scores run two blocks ahead.  Warps: 0-3 and
 // 4-7 elementwise (keys 0-63 and 64-127 of a block), 8 loads, 9 issues S, 10
-// dP, 11 dQ.
+// dP, 11 dQ.  About 2150 clk a block (window_bwd_wan5b: 680 us): 64 KB of K and V
+// have to enter shared memory for 1536 clk of MMA that read it too.  The
+// warpgroups on alternate blocks instead: 725 us.
 template <int D, bool F16>
 __global__ void __launch_bounds__(kWbThreads, 1)
     window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
@@ -391,7 +393,7 @@ enum : int {
 // warps finish dS.  P^T is released in two parts, so dV starts before the
 // exponentials end.  Warps: 0-7 elementwise, 8 loads, 9 fetches LSE and delta
 // of the walked queries, 10 issues S and dV, 11 dP and dK.
-template <int D, bool F16>
+template <int D, bool F16, bool SHARED>
 __global__ void __launch_bounds__(kWbThreads, 1)
     window_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
                       const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -411,10 +413,15 @@ __global__ void __launch_bounds__(kWbThreads, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int hk = blockIdx.y, b = blockIdx.z;
   // first keys first: they may be seen by every query
-  const int x = blockIdx.x - ds.heavy * ds.sh;
-  const bool hv = x < 0;
-  const int S = hv ? ds.sh : ds.sn;                    // CTAs of this key block
-  const int blk = hv ? blockIdx.x / S : ds.heavy + x / S, sp_i = hv ? blockIdx.x % S : x % S;
+  int blk = blockIdx.x, S = 1, sp_i = 0, x = 0;        // S: CTAs of this key block (SHARED: some have several)
+  bool hv = false;
+  if (SHARED) {
+    x = blockIdx.x - ds.heavy * ds.sh;
+    hv = x < 0;
+    S = hv ? ds.sh : ds.sn;
+    blk = hv ? blockIdx.x / S : ds.heavy + x / S;
+    sp_i = hv ? blockIdx.x % S : x % S;
+  }
   const int c0 = blk * kWbRows;
   const int len = win_len(a, b), start = win_start(a, b, len);
   // queries that see some key of [c0, c1): one range of rows, [qlo, qhi)
@@ -430,8 +437,8 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     }
   }
   const int n_all = nq * a.group;
-  const int j0 = static_cast<int>(static_cast<long long>(n_all) * sp_i / S);
-  const int n = static_cast<int>(static_cast<long long>(n_all) * (sp_i + 1) / S) - j0;   // this CTA's walk
+  const int j0 = SHARED ? static_cast<int>(static_cast<long long>(n_all) * sp_i / S) : 0;
+  const int n = SHARED ? static_cast<int>(static_cast<long long>(n_all) * (sp_i + 1) / S) - j0 : n_all;   // this CTA's walk
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
@@ -454,7 +461,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t tS = tmem, tDP = tmem + 128, tDV = tmem + 256, tDK = tmem + 384;
   // walked block j: query head hk * group + (j0 + j) / nq, rows from (qb0 + (j0 + j) % nq) * 128
-  const int h_first = hk * a.group + (nq > 0 ? j0 / nq : 0), q_first = nq > 0 ? j0 % nq : 0;
+  const int h_first = hk * a.group + (SHARED && nq > 0 ? j0 / nq : 0), q_first = SHARED && nq > 0 ? j0 % nq : 0;
 
   if (warp == 8) {
     // ====================================================== TMA producer
@@ -706,7 +713,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       mbar_arrive(bar(DK_ST_EMPTY + st));
     }
     // ---- epilogue: warpgroup 0 writes dV through V's buffer, 1 dK through K's
-    if (S > 1) {
+    if (SHARED && S > 1) {
       if (n > 0 && ok)
         ok = __all_sync(0xffffffffu, mbar_wait(bar(DK_OUT), 0, abort_flag, a.err) &&
                                          mbar_wait(bar(DK_OUT + 1), 0, abort_flag, a.err));
