@@ -77,6 +77,7 @@ static int encode_heads(CUtensorMap* m, const void* ptr, int B, int N, int H, in
 // when its CTAs are too few, as far as the most keys that a row can see allow
 // (the lengths are on the device).
 constexpr int kWsMaxRows = 64;
+constexpr int kWfFixed = 6;
 // CTAs that a step call asks for, two an SM: with splits joined in a cluster 1.5
 // rounds of them (64 row tiles of 16384 keys: 5 splits 127 us, 7 95 us, 8 94 us,
 // 18 and a second kernel 104 us; 256 tiles of 2048: 2 splits 51 us, 8 84 us), with
@@ -93,18 +94,37 @@ static WinPlan win_plan(const WinArgs& a) {
   WinPlan p;
   const long long rows = 1ll * a.Nq * a.group;
   p.step = rows <= kWsMaxRows && a.Hkv * ((rows + kWsRows - 1) / kWsRows) <= 65535;      // (grid.y)
-  const long long keys = std::min<long long>(
-      a.Nk, std::min(a.sink_tok, 1ll << 32) + std::min((a.window + 1ll) * a.unit, 1ll << 32) + a.Nq);
+  // the most keys that `span` consecutive queries see
+  auto keys_of = [&](long long span) {
+    return std::min<long long>(
+        a.Nk, std::min(a.sink_tok, 1ll << 32) + std::min((a.window + 1ll) * a.unit, 1ll << 32) + span);
+  };
   if (p.step) {
     const long long ctas = 1ll * a.B * a.Hkv * ((rows + kWsRows - 1) / kWsRows);
-    const long long most = std::max(1ll, keys / (kWsKeys * kWsWarps * 2));   // two tiles a warp at least
+    const long long most = std::max(1ll, keys_of(a.Nq) / (kWsKeys * kWsWarps * 2));   // two tiles a warp at least
     const long long want = std::min((kWsClusterCtas + ctas - 1) / ctas, most);
     p.cluster = want <= kWsCluster;
     p.splits = static_cast<int>(std::max(1ll, p.cluster ? want : std::min({(kWsSplitCtas + ctas - 1) / ctas, most, 256ll})));
     if (p.splits == 1) p.cluster = false;
   } else {
+    // Splits s that make rounds * (blocks of a split + kWfFixed) least: the rounds
+    // of CTAs that the SMs take, and what starting and ending a CTA costs in
+    // blocks' time (about 10k clk of ~1.7k).  Writing and reading partial results
+    // comes on top, so a split has to save a fifth (24 heads, 880 queries, 94
+    // blocks: 209 us in one round of 96 CTAs, 232 us as three splits in two; 6
+    // heads, 160 blocks: 271 us, 82 us with 6 splits).
     p.cluster = false;
     p.splits = 1;
+    const long long ctas = 1ll * ((a.Nq + kWfRows - 1) / kWfRows) * a.Hq * a.B;
+    const long long blocks = (keys_of(kWfRows) + kWfKeys - 1) / kWfKeys;
+    long long best = (ctas + 147) / 148 * (blocks + kWfFixed) * 4 / 5;
+    for (long long s = 2; s <= 8 && s * 4 <= blocks && a.B * s <= 65535; ++s) {
+      const long long cost = (ctas * s + 147) / 148 * ((blocks + s - 1) / s + kWfFixed) + kWfFixed;
+      if (cost < best) {
+        best = cost;
+        p.splits = static_cast<int>(s);
+      }
+    }
   }
   return p;
 }

@@ -23,16 +23,17 @@
 // complete and O may be rescaled (only when a row's maximum grew by more than
 // 2^8).
 //
-// A block's cycle (clock stamps, d = 128): scores seen, 90 clk to load them,
-// 560 for the maximum and the first 32 keys' P, 3 x 540 for the others, then
-// the last P V and the next S: 3.4-3.7k clk for two 128 x 128 blocks (2048 of
-// MMA).  window_wan5b (6 heads of 27280 tokens, 8 frames and a sink): 575 us in
-// bursts (1005 TFLOP/s, 62 % of the measured peak), 600 us under the power cap.
+// Left alone, the slots fall into step: both softmaxes at once, sharing the
+// exponential unit, then both waiting for MMAs (3.4-3.7k clk for two 128 x 128
+// blocks, 2048 of MMA).  So at d = 128 they take turns (window_wan5b 592 -> 540
+// us; at d = 64, where the products are half as long, turns cost 4 %).
+// window_wan5b, 6 heads of 27280 tokens, 8 frames and a sink: 540 us in bursts
+// (1070 TFLOP/s, 66 % of the measured peak), 550 us under the power cap.
 // Measured and not taken: a warpgroup on each half of a block's keys (four
 // softmax warps a sub-partition, row maxima joined by an OR barrier) 8 %
-// slower; 1/8 to 3/8 of the exponentials on the FMA pipe 4 to 10 % slower; the
+// slower; 1/8 to 3/8 of the exponentials on the FMA pipe 2 to 10 % slower; the
 // maximum before any exponential, P released in halves and the next S issued
-// after a K wait 8 % slower.
+// after a K wait 8 % slower; at d = 64 one slot a CTA and two CTAs an SM equal.
 //
 // Rounding: P is rounded to the 16-bit input type for the P V MMA (its sum l
 // is taken from the float32 values), O once at the end.
@@ -56,7 +57,7 @@ struct WfSmem {
   static constexpr int kSlab = 128 * 128;              // 128 rows x 64 channels
   static constexpr int kSlabs = D / 64;
   static constexpr int kBuf = kSlabs * kSlab;          // 128 rows
-  static constexpr int kKSt = D == 128 ? 3 : 4, kVSt = D == 128 ? 2 : 4;
+  static constexpr int kKSt = 3, kVSt = 2;
   static constexpr int kQ = 0;                         // two slots; O leaves through them
   static constexpr int kK = 2 * kBuf;
   static constexpr int kV = kK + kKSt * kBuf;
@@ -306,21 +307,32 @@ __global__ void __launch_bounds__(kWfThreads, 1)
     if (i < a.Nq) vis = row_vis(a, len, start + i);
     float m = -INFINITY, l = 0.f;
     int c = 0;
+    // After a wait that gave up (ok = false) the loop goes on without waiting, so
+    // that both slots meet at every hand-over.
     bool ok = true;
+    // The slots take turns: slot 0's exponentials of a block, then slot 1's, and
+    // so on (named barriers 3 and 4, a turn a block whether the slot uses it or
+    // not); the turn is passed on after half of them.
+    constexpr bool kTurns = D == 128;
+    if (kTurns && s == 1 && n > 0) named_bar_arrive(3, 256);
     const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2);
     for (int j = 0; j < n; ++j) {
       const int blk = wb.block(it0 + j), c0 = blk * kWfKeys;
-      if (!mine.has(blk)) continue;
+      const bool pass = s == 0 || j < n - 1;           // (slot 0 waits once less than slot 1 has turns)
+      if (!mine.has(blk)) {
+        if (kTurns) {
+          named_bar_sync(3 + s, 256);
+          if (pass) named_bar_arrive(4 - s, 256);
+        }
+        continue;
+      }
       const bool row_full = i >= a.Nq || c0 + kWfKeys <= vis.first || (c0 >= vis.lo && c0 + kWfKeys <= vis.hi);
       const bool masked = __any_sync(0xffffffffu, !row_full);
       // Keys of the block that no row of the CTA sees may hold anything: zero
       // their V rows (0 * NaN would reach O).  Both slots write the same zeros.
       if ((c0 + kWfKeys > wb.hi || c0 < wb.lo) && c0 + kWfKeys > wb.first) {
         const int vs = j % L::kVSt, key = c0 + r;
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(WB_V_FULL + vs), (j / L::kVSt) & 1, abort_flag, a.err))) {
-          ok = false;
-          break;
-        }
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(WB_V_FULL + vs), (j / L::kVSt) & 1, abort_flag, a.err));
         if (key >= wb.first && (key < wb.lo || key >= wb.hi)) {
           const uint32_t row = base + L::kV + vs * L::kBuf + r * 128u;
 #pragma unroll
@@ -330,10 +342,7 @@ __global__ void __launch_bounds__(kWfThreads, 1)
         }
         fence_proxy_async_smem();
       }
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(WB_S + s), c & 1, abort_flag, a.err))) {
-        ok = false;
-        break;
-      }
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(WB_S + s), c & 1, abort_flag, a.err));
       tc_fence_after();
       uint32_t x[128];
       tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
@@ -371,6 +380,7 @@ __global__ void __launch_bounds__(kWfThreads, 1)
       };
       uint32_t pk[16];
       float mu = m == -INFINITY ? 0.f : m;
+      if (kTurns) named_bar_sync(3 + s, 256);
       expo(0, f2_pack(-mu, -mu), pk);
       const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
       sched_fence(a);
@@ -402,6 +412,7 @@ __global__ void __launch_bounds__(kWfThreads, 1)
 #pragma unroll
       for (int q = 1; q < 4; ++q) {
         expo(32 * q, nm2, pk);
+        if (kTurns && q == 1 && pass) named_bar_arrive(4 - s, 256);
         tmem_st16(tS + 16u * q, pk);
         tmem_wait_st();
         tc_fence_before();
