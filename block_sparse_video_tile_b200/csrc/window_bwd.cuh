@@ -100,15 +100,6 @@ __device__ __forceinline__ void stage_row(uint32_t t, uint32_t buf, int r, float
   }
 }
 
-// Zeros row r of a 128-row tile.
-template <int D>
-__device__ __forceinline__ void zero_row(uint32_t buf, int r) {
-#pragma unroll
-  for (int sl = 0; sl < D / 64; ++sl)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) st_shared_v4(buf + sl * WbSmem<D>::kSlab + r * 128u + e * 16u, 0u, 0u, 0u, 0u);
-}
-
 // ------------------------------------------------------------------ dQ
 enum : int {
   DQ_OWN = 0, DQ_S = 1 /* [2] */, DQ_DP = 3, DQ_DP_FREE = 4, DQ_DS = 5 /* [2] */, DQ_S_FREE = 7 /* [2] */, DQ_OUT = 9,
@@ -294,12 +285,12 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       // Keys that no row of the CTA sees may hold anything: zero their K rows
       // (0 * NaN would reach dQ).
       if ((c0 + kWfKeys > wb.hi || c0 < wb.lo) && c0 + kWfKeys > wb.first) {
-        const int ks = j % L::kASt, key = c0 + r;
+        const int ks = j % L::kASt;
         if (!__all_sync(0xffffffffu, mbar_wait(bar(DQ_K_FULL + ks), (j / L::kASt) & 1, abort_flag, a.err))) {
           ok = false;
           break;
         }
-        if (w == 0 && key >= wb.first && (key < wb.lo || key >= wb.hi)) zero_row<D>(base + L::kA + ks * L::kBuf, r);
+        if (w == 0) zero_unseen<D>(base + L::kA + ks * L::kBuf, c0, wb.first, wb.lo, wb.hi, r);
         fence_proxy_async_smem();
       }
       if (!__all_sync(0xffffffffu, mbar_wait(bar(DQ_S + sb), (j >> 1) & 1, abort_flag, a.err))) {
@@ -631,9 +622,15 @@ __global__ void __launch_bounds__(kWbThreads, 1)
           ok = false;
           break;
         }
-        const RowVis v = row_vis(a, len, start + i0 + r);
-        if (v.hi == v.lo && v.first == 0 && i0 + r < a.Nq)
-          zero_row<D>(base + (w == 0 ? L::kA + (j % L::kASt) * L::kBuf : L::kB + st * L::kBuf), r);
+        // the live rows are those from position 0 on whose window begins before the end
+        // of the keys (with first units, all of them); one range of the block
+        const int at0 = max(0, -(start + i0));
+        int n_live = 0;
+        for (int e = lane; e < kWbRows; e += 32) {
+          const RowVis v = row_vis(a, len, start + i0 + e);
+          n_live += __popc(__ballot_sync(0xffffffffu, v.hi > v.lo || v.first > 0));
+        }
+        zero_unseen<D>(base + (w == 0 ? L::kA + (j % L::kASt) * L::kBuf : L::kB + st * L::kBuf), 0, 0, at0, at0 + n_live, r);
         fence_proxy_async_smem();
       }
       if (!__all_sync(0xffffffffu, mbar_wait(bar(DK_ST_FULL + st), (j >> 1) & 1, abort_flag, a.err) &&
