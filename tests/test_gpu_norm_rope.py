@@ -222,3 +222,37 @@ def test_large_call_against_torch():
     terms = back * un
     # a lane adds at most ceil(495 groups / 592 CTAs) * 24 rows, then 16 + 8 + 592 / 8 + 8 partial sums
     assert ((dw.double() - terms.sum((0, 1, 2))).abs() <= 256 * 2.0 ** -24 * terms.abs().sum((0, 1, 2))).all()
+
+
+def test_offsets_beyond_32_bits():
+    """Two videos further apart than 2^31 elements."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    N, H, d, grid = 24, 3, 128, (2, 3, 4)
+    far = (1 << 31) + 64
+    room = torch.zeros(far + N * H * d, dtype=torch.bfloat16, device="cuda")
+    q = room.as_strided((2, N, H, d), (far, H * d, d, 1))
+    q.copy_(rand(g, 2, H, N, d, "bf16", "bnhd"))
+    kw = dict(table=api.rope_table(grid, d), q_weight=torch.rand(d, device="cuda", generator=g), layout="bnhd")
+    near = q.contiguous()
+    assert torch.equal(api.qk_norm_rope(q, None, grid, **kw)[0], api.qk_norm_rope(near, None, grid, **kw)[0])
+    a, b = (api.qk_norm_rope_bwd(x, None, x, None, grid, **kw) for x in (q, near))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[2], b[2])
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_gradient_against_differences(interleaved):
+    """dx and dw against central differences of the call's own result along the gradient (fp16; the rounding of y, 2^-11
+    of a value, is a random 1e-4 of the rise that it hides; the curvature of a step of 0.1 about 1 %)."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    grid, d = (2, 3, 5), 64
+    x, dy = rand(g, 1, 4, 30, d, "f16", "bhnd", 1.5), rand(g, 1, 4, 30, d, "f16", "bhnd")
+    w = 1 + 0.1 * torch.randn(d, generator=g, device="cuda")
+    kw = dict(table=api.rope_table(grid, d), interleaved=interleaved)
+    dx, _, dw, _ = api.qk_norm_rope_bwd(dy, None, x, None, grid, q_weight=w, **kw)
+    for gr, at, f in ((dx, x, lambda t: api.qk_norm_rope(t, None, grid, q_weight=w, **kw)[0]),
+                      (dw, w, lambda t: api.qk_norm_rope(x, None, grid, q_weight=t, **kw)[0])):
+        step = gr.double() / gr.double().abs().max()
+        a, b = ((at.double() + sign * 0.1 * step).to(at.dtype) for sign in (1, -1))
+        rise = ((f(a).double() - f(b).double()) * dy.double()).sum()
+        slope = ((a.double() - b.double()) * gr.double()).sum()
+        assert abs(rise - slope) <= 0.03 * abs(slope)

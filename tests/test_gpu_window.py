@@ -50,6 +50,11 @@ CASES = {
     "frames_no_sink": c(1, 2, 1, 700, 700, 64, 1, 0, 100, layout="bnhd"),
     "frames_chunk": c(1, 3, 3, 176, 880, 128, 3, 2, 88, layout="bnhd"),
     "frame_over_everything": c(1, 2, 2, 300, 300, 128, 1, 0, 4096),
+    "long_frames": c(1, 2, 1, 1500, 1500, 64, 1, 0, 500),
+    "long_frames_sink": c(1, 1, 1, 1300, 1300, 128, 2, 1, 350, layout="bnhd", kv_len=[1290]),
+    "few_ctas": c(1, 1, 1, 100, 3000, 128, 2900, 5),
+    "few_ctas_64": c(1, 2, 1, 130, 2500, 64, 3000, 0, dtype="f16", layout="bnhd"),
+    "sinks_seen_by_all": c(1, 4, 1, 1100, 1100, 64, 40, 3, layout="bnhd"),
     "partial_frames": c(2, 2, 2, 130, 530, 128, 2, 1, 130, kv_len=[530, 399]),
     "ragged": c(3, 2, 2, 300, 400, 128, 90, 5, kv_len=[400, 0, 131]),
     "fewer_keys_than_queries": c(2, 2, 2, 300, 300, 64, 60, 2, kv_len=[40, 300], dtype="f16"),
@@ -77,6 +82,9 @@ def make(case, seed=0, poison=True):
         for b in range(B):
             for x, bad in ((k, float("nan")), (v, float("inf"))):
                 (x[b].transpose(0, 1) if layout == "bhnd" else x[b])[lens[b]:] = bad
+            gone = torch.from_numpy(~sees[b].any(0)).cuda()          # between first units and window, too
+            (k[b].transpose(0, 1) if layout == "bhnd" else k[b])[gone] = float("inf")
+            (v[b].transpose(0, 1) if layout == "bhnd" else v[b])[gone] = float("nan")
             dead = torch.from_numpy(~sees[b].any(1)).cuda()
             for x in (q, do):
                 (x[b].transpose(0, 1) if layout == "bhnd" else x[b])[dead] = float("nan")
@@ -291,3 +299,69 @@ def test_block_sparse_forward_with_norm_rope():
     got = api.forward(q, k, v, grid, tile, 3, layout="bnhd", norm_rope=how)
     q2, k2 = api.qk_norm_rope(q, k, grid, layout="bnhd", **how)
     assert all(torch.equal(a, b) for a, b in zip(got, api.forward(q2, k2, v, grid, tile, 3, layout="bnhd")))
+
+
+@pytest.mark.parametrize("Nq", [1, 5, 200])
+def test_cache_beyond_32_bit_offsets(Nq):
+    """The window lies behind 2^31 elements of the cache; the answer is that of a short copy (whose keys may be split
+    and blocked differently: each within its bound)."""
+    H, d, Nk, tail = 8, 128, (1 << 21) + 4096, 1024
+    g = torch.Generator(device="cuda").manual_seed(8)
+    k, v = (torch.empty(1, Nk, H, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for x in (k, v):
+        x[:, -tail:] = torch.randn(1, tail, H, d, generator=g, device="cuda").bfloat16()
+    q = rand(g, 1, H, Nq, d, "bf16", "bnhd")
+    o, lse = api.window_attn(q, k, v, 300, layout="bnhd")
+    ks, vs = k[:, -tail:].contiguous(), v[:, -tail:].contiguous()
+    ref = api.window_attn(q, ks, vs, 300, layout="bnhd")
+    sees = [lo.visible(Nq, tail, tail, tail - Nq, 300, 0, 1)]
+    _, _, bo, bl = lo.window_fwd(*(bhnd(x, "bnhd") for x in (q, ks, vs)), sees, d ** -0.5, 2.0 ** -8)
+    within(bhnd(o, "bnhd"), bhnd(ref[0], "bnhd"), 2 * bo, "O")
+    within(f64(lse), f64(ref[1]), 2 * bl, "LSE")
+    if Nq == 200:
+        do = rand(g, 1, H, Nq, d, "bf16", "bnhd")
+        got = api.window_attn_bwd(do, q, k, v, o, lse, 300, layout="bnhd")
+        want = api.window_attn_bwd(do, q, ks, vs, *ref, 300, layout="bnhd")
+        _, tol = lo.window_bwd(*(bhnd(x, "bnhd") for x in (do, q, ks, vs)), sees, d ** -0.5, 2.0 ** -8)
+        for what, a, b, t in zip(("dq", "dk", "dv"), (got[0], got[1][:, -tail:], got[2][:, -tail:]), want, tol):
+            within(bhnd(a, "bnhd"), bhnd(b, "bnhd"), 2 * t, what)
+        assert not got[1][:, :-tail].any() and not got[2][:, :-tail].any()
+
+
+def test_two_streams_at_once():
+    g = torch.Generator(device="cuda").manual_seed(9)
+    calls = []
+    for Nq in (1, 333):
+        q, k, v = rand(g, 2, 4, Nq, 128, "bf16", "bhnd"), *(rand(g, 2, 2, 5000, 128, "bf16", "bhnd") for _ in range(2))
+        calls.append((q, k, v))
+    want = [api.window_attn(*c, 4000, sink=3) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = [api.window_attn(*calls[i % 2], 4000, sink=3, stream=streams[i % 4]) for i in range(24)]
+    torch.cuda.synchronize()
+    for i, r in enumerate(got):
+        assert torch.equal(r[0], want[i % 2][0]) and torch.equal(r[1], want[i % 2][1])
+
+
+def test_gradient_against_differences():
+    """dq, dk and dv against central differences of the call's own O (fp16 inputs moved by a step h that fp16 holds
+    exactly).  O is rounded to fp16 (2^-11 of a value, and P's rounding the same), so a difference of sums over n values
+    is off by at most (2 * 2^-11 * sum |o do|) / (2 h) -- far too much for one entry; averaged over a random direction
+    of all entries it is that divided by about sqrt(n) while the derivative along it grows with the norm, so whole
+    directions are compared, to 3 %."""
+    g = torch.Generator(device="cuda").manual_seed(10)
+    q, k, v = rand(g, 1, 4, 200, 64, "f16", "bhnd"), *(rand(g, 1, 2, 200, 64, "f16", "bhnd") for _ in range(2))
+    do = rand(g, 1, 4, 200, 64, "f16", "bhnd")
+    kw = dict(window=2, sink=1, unit=40)
+    o, lse = api.window_attn(q, k, v, **kw)
+    grads = api.window_attn_bwd(do, q, k, v, o, lse, **kw)
+    for i, gr in enumerate(grads):
+        step = gr.double() / gr.double().abs().max()                # along the gradient: the largest derivative
+        args = [q, k, v]
+        ends = []
+        for sign in (1, -1):
+            moved = (args[i].double() + sign * 0.25 * step).half()
+            ends.append((moved.double(), api.window_attn(*(moved if j == i else x for j, x in enumerate(args)), **kw)[0]))
+        rise = ((ends[0][1].double() - ends[1][1].double()) * do.double()).sum()
+        slope = ((ends[0][0] - ends[1][0]) * gr.double()).sum()      # the steps as fp16 took them
+        assert abs(rise - slope) <= 0.03 * abs(slope), (i, float(rise), float(slope))
