@@ -5,7 +5,7 @@ from __future__ import annotations
 import torch
 
 from ._native import VsaNormRope, VsaQkSide, check, lib
-from ._strided import AXES, DTYPES, Plans, apart, dims, head_tensor, on, sig, strides
+from ._strided import AXES, DTYPES, Plans, apart, dims, empty_f32, head_tensor, on, sig, strides
 
 __all__ = ["rope_split", "rope_table", "qk_norm_rope", "qk_norm_rope_bwd"]
 
@@ -115,14 +115,14 @@ def qk_norm_rope(q, k, grid, *, table=None, table_k=None, q_weight=None, k_weigh
         apart([("out", y) for y in out if y is not None],
               [(n, x) for n, x in (("q", q), ("k", k), ("table", table), ("q_weight", q_weight), ("k_weight", k_weight))
                if x is not None])
-    with on(device, stream, (q, k, table, table_k, q_weight, k_weight) + tuple(out or ())) as st:
+    def run(st):
         call, outs = [], []
         for i, (side, x, t, w) in enumerate(((sides[0], q, table, q_weight),
                                              (sides[1], k, table if table_k is None else table_k, k_weight))):
             if side is None:
                 outs.append(None)
                 continue
-            y = x.new_empty(side[1]) if out is None else out[i]
+            y = x.new_empty(*side[1]) if out is None else out[i]
             outs.append(y)
             if side[0] is None:
                 continue
@@ -137,7 +137,9 @@ def qk_norm_rope(q, k, grid, *, table=None, table_k=None, q_weight=None, k_weigh
             call.append(c)
         if call:
             check("vsa_qk_norm_rope", lib().vsa_qk_norm_rope(p, call[0], call[1] if len(call) > 1 else None, st))
-    return outs[0], outs[1]
+        return outs[0], outs[1]
+
+    return on(device, stream, (q, k, table, table_k, q_weight, k_weight, *(out or ())), run)
 
 
 def qk_norm_rope_bwd(dq_out, dk_out, q, k, grid, *, table=None, table_k=None, q_weight=None, k_weight=None,
@@ -152,7 +154,7 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, grid, *, table=None, table_k=None, q_
             q_weight, k_weight, (dq_out, dk_out))
     p, sides = _plan(_key(*args), *args)
     device = q.device
-    with on(device, stream, (q, k, dq_out, dk_out, table, table_k, q_weight, k_weight)) as st:
+    def run(st):
         call, dx, dw = [], [], []
         for side, x, dy, t, w in ((sides[0], q, dq_out, table, q_weight),
                                   (sides[1], k, dk_out, table if table_k is None else table_k, k_weight)):
@@ -160,8 +162,8 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, grid, *, table=None, table_k=None, q_
                 dx.append(None)
                 dw.append(None)
                 continue
-            gx = x.new_empty(side[1])
-            gw = None if w is None else torch.empty(p.d, dtype=torch.float32, device=device)
+            gx = x.new_empty(*side[1])
+            gw = None if w is None else empty_f32(device, p.d)
             dx.append(gx)
             dw.append(gw)
             if side[0] is None:
@@ -178,6 +180,8 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, grid, *, table=None, table_k=None, q_
         if call:
             sk = call[1] if len(call) > 1 else None
             n = lib().vsa_qk_norm_rope_bwd_workspace_bytes(p, call[0], sk)
-            ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+            ws = empty_f32(device, (n + 3) // 4) if n else None
             check("vsa_qk_norm_rope_bwd", lib().vsa_qk_norm_rope_bwd(p, call[0], sk, ws.data_ptr() if n else None, n, st))
-    return dx[0], dx[1], dw[0], dw[1]
+        return dx[0], dx[1], dw[0], dw[1]
+
+    return on(device, stream, (q, k, dq_out, dk_out, table, table_k, q_weight, k_weight), run)

@@ -7,7 +7,7 @@ import math
 import torch
 
 from ._native import VsaWindow, check, lib
-from ._strided import AXES, DTYPES, Plans, apart, dims, head_tensor, on, sig, strides
+from ._strided import AXES, DTYPES, Plans, apart, dims, empty_f32, head_tensor, on, sig, strides
 
 __all__ = ["window_attn", "window_attn_bwd"]
 
@@ -93,28 +93,31 @@ def window_attn(q, k, v, window: int, *, sink: int = 0, unit: int = 1, kv_len=No
         if lse is not None:
             _check_lse(lse, (B, t.Hq, t.Nq), device)
         apart([(name, x) for name, x in (("out", out), ("lse", lse)) if x is not None], [("q", q), ("k", k), ("v", v)])
-    with on(device, stream, (q, k, v, _tensor(kv_len), _tensor(q_start), out, lse)) as st:
+    def run(st):
         n = _positions("kv_len", kv_len, 0, Nk, B, device)
         p0 = _positions("q_start", q_start, -_MAX_POS, _MAX_POS, B, device)
         w = VsaWindow.from_buffer_copy(t)
         if out is None:
-            out = q.new_empty(oshape)
+            o = q.new_empty(*oshape)
         else:
-            w.o_s = strides(out, layout)
-        if lse is None:
-            lse = torch.empty((B, w.Hq, w.Nq), dtype=torch.float32, device=device)
-        if not (B and w.Nq and w.Hq):
-            return out, lse
-        if not (Nk and w.Hkv):
-            return out.zero_(), lse.fill_(-math.inf)
+            o = out
+            w.o_s = strides(o, layout)
+        ls = empty_f32(device, B, t.Hq, t.Nq) if lse is None else lse
+        if not (B and t.Nq and t.Hq):
+            return o, ls
+        if not (Nk and t.Hkv):
+            return o.zero_(), ls.fill_(-math.inf)
         if n is not None:
             w.kv_len = n.data_ptr()
         if p0 is not None:
             w.q_start = p0.data_ptr()
-        ws = torch.empty(size, dtype=torch.uint8, device=device).data_ptr() if size else None
+        ws = empty_f32(device, (size + 3) // 4) if size else None
         check("vsa_window_attn", lib().vsa_window_attn(
-            w, q.data_ptr(), k.data_ptr(), v.data_ptr(), scale, out.data_ptr(), lse.data_ptr(), ws, size, st))
-    return out, lse
+            w, q.data_ptr(), k.data_ptr(), v.data_ptr(), scale, o.data_ptr(), ls.data_ptr(),
+            ws.data_ptr() if size else None, size, st))
+        return o, ls
+
+    return on(device, stream, (q, k, v, _tensor(kv_len), _tensor(q_start), out, lse), run)
 
 
 def window_attn_bwd(do, q, k, v, out, lse, window: int, *, sink: int = 0, unit: int = 1, kv_len=None, q_start=None,
@@ -124,10 +127,10 @@ def window_attn_bwd(do, q, k, v, out, lse, window: int, *, sink: int = 0, unit: 
     zeros.  Every sum has a fixed order (the same bits each time)."""
     t, oshape, kshape, scale, size = _plan(q, k, v, window, sink, unit, layout, scale, do, out, lse)
     device, B = q.device, t.B
-    with on(device, stream, (do, q, k, v, out, lse, _tensor(kv_len), _tensor(q_start))) as st:
+    def run(st):
         n = _positions("kv_len", kv_len, 0, t.Nk, B, device)
         p0 = _positions("q_start", q_start, -_MAX_POS, _MAX_POS, B, device)
-        dq, dk, dv = q.new_empty(oshape), k.new_empty(kshape), k.new_empty(kshape)
+        dq, dk, dv = q.new_empty(*oshape), k.new_empty(*kshape), k.new_empty(*kshape)
         if not (B and t.Nq and t.Hq and t.Nk and t.Hkv):
             return dq.zero_(), dk.zero_(), dv.zero_()
         w = VsaWindow.from_buffer_copy(t)
@@ -135,8 +138,10 @@ def window_attn_bwd(do, q, k, v, out, lse, window: int, *, sink: int = 0, unit: 
             w.kv_len = n.data_ptr()
         if p0 is not None:
             w.q_start = p0.data_ptr()
-        ws = torch.empty(size, dtype=torch.uint8, device=device)
+        ws = empty_f32(device, (size + 3) // 4)
         check("vsa_window_attn_bwd", lib().vsa_window_attn_bwd(
             w, do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), scale,
             dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), size, st))
-    return dq, dk, dv
+        return dq, dk, dv
+
+    return on(device, stream, (do, q, k, v, out, lse, _tensor(kv_len), _tensor(q_start)), run)
