@@ -92,6 +92,20 @@ def _key(q, k, grid, grid_k, split, eps, interleaved, layout, table, table_k, q_
             sig(table_k), sig(q_weight), sig(k_weight), None if dy is None else (sig(dy[0]), sig(dy[1])))
 
 
+def _side(side, x, y, t, w):
+    """A side's argument structure with its addresses (None where it has no rows)."""
+    if side is None or side[0] is None:
+        return None
+    c = VsaQkSide.from_buffer_copy(side[0])
+    c.x = x.data_ptr()
+    c.y = y.data_ptr()
+    if w is not None:
+        c.weight = w.data_ptr()
+    if t is not None:
+        c.table = t.data_ptr()
+    return c
+
+
 def qk_norm_rope(q, k, grid, *, table=None, table_k=None, q_weight=None, k_weight=None, eps: float = 1e-6,
                  split=None, grid_k=None, interleaved: bool = True, layout: str = "bhnd", out=None, stream=None):
     """(q', k') = rotation of the RMS-normed rows of q and k, for each token and head:
@@ -116,28 +130,19 @@ def qk_norm_rope(q, k, grid, *, table=None, table_k=None, q_weight=None, k_weigh
               [(n, x) for n, x in (("q", q), ("k", k), ("table", table), ("q_weight", q_weight), ("k_weight", k_weight))
                if x is not None])
     def run(st):
-        call, outs = [], []
-        for i, (side, x, t, w) in enumerate(((sides[0], q, table, q_weight),
-                                             (sides[1], k, table if table_k is None else table_k, k_weight))):
-            if side is None:
-                outs.append(None)
-                continue
-            y = x.new_empty(*side[1]) if out is None else out[i]
-            outs.append(y)
-            if side[0] is None:
-                continue
-            c = VsaQkSide.from_buffer_copy(side[0])
-            c.x, c.y = x.data_ptr(), y.data_ptr()
-            if out is not None:
-                c.y_s = strides(y, layout)
-            if w is not None:
-                c.weight = w.data_ptr()
-            if t is not None:
-                c.table = t.data_ptr()
-            call.append(c)
-        if call:
-            check("vsa_qk_norm_rope", lib().vsa_qk_norm_rope(p, call[0], call[1] if len(call) > 1 else None, st))
-        return outs[0], outs[1]
+        sq, sk = sides
+        yq, yk = out if out is not None else (q.new_empty(*sq[1]), None if sk is None else k.new_empty(*sk[1]))
+        cq = _side(sq, q, yq, table, q_weight)
+        ck = _side(sk, k, yk, table if table_k is None else table_k, k_weight)
+        if out is not None:
+            for c, y in ((cq, yq), (ck, yk)):
+                if c is not None:
+                    c.y_s = strides(y, layout)
+        if cq is None:
+            cq, ck = ck, None
+        if cq is not None:
+            check("vsa_qk_norm_rope", lib().vsa_qk_norm_rope(p, cq, ck, st))
+        return yq, yk
 
     return on(device, stream, (q, k, table, table_k, q_weight, k_weight, *(out or ())), run)
 
@@ -154,34 +159,30 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, grid, *, table=None, table_k=None, q_
             q_weight, k_weight, (dq_out, dk_out))
     p, sides = _plan(_key(*args), *args)
     device = q.device
-    def run(st):
-        call, dx, dw = [], [], []
-        for side, x, dy, t, w in ((sides[0], q, dq_out, table, q_weight),
-                                  (sides[1], k, dk_out, table if table_k is None else table_k, k_weight)):
-            if side is None:
-                dx.append(None)
-                dw.append(None)
-                continue
-            gx = x.new_empty(*side[1])
-            gw = None if w is None else empty_f32(device, p.d)
-            dx.append(gx)
-            dw.append(gw)
-            if side[0] is None:
-                if gw is not None:
-                    gw.zero_()
-                continue
-            c = VsaQkSide.from_buffer_copy(side[0])
-            c.x, c.y, c.dx = x.data_ptr(), dy.data_ptr(), gx.data_ptr()
+    def grad(side, x, dy, t, w):
+        """(argument structure, dx, dweight) of a side."""
+        if side is None:
+            return None, None, None
+        gx = x.new_empty(*side[1])
+        gw = None if w is None else empty_f32(device, p.d)
+        c = _side(side, x, dy, t, w)
+        if c is not None:
+            c.dx = gx.data_ptr()
             if w is not None:
-                c.weight, c.dweight = w.data_ptr(), gw.data_ptr()
-            if t is not None:
-                c.table = t.data_ptr()
-            call.append(c)
-        if call:
-            sk = call[1] if len(call) > 1 else None
-            n = lib().vsa_qk_norm_rope_bwd_workspace_bytes(p, call[0], sk)
+                c.dweight = gw.data_ptr()
+        elif gw is not None:
+            gw.zero_()
+        return c, gx, gw
+
+    def run(st):
+        cq, gq, gwq = grad(sides[0], q, dq_out, table, q_weight)
+        ck, gk, gwk = grad(sides[1], k, dk_out, table if table_k is None else table_k, k_weight)
+        if cq is None:
+            cq, ck = ck, None
+        if cq is not None:
+            n = lib().vsa_qk_norm_rope_bwd_workspace_bytes(p, cq, ck)
             ws = empty_f32(device, (n + 3) // 4) if n else None
-            check("vsa_qk_norm_rope_bwd", lib().vsa_qk_norm_rope_bwd(p, call[0], sk, ws.data_ptr() if n else None, n, st))
-        return dx[0], dx[1], dw[0], dw[1]
+            check("vsa_qk_norm_rope_bwd", lib().vsa_qk_norm_rope_bwd(p, cq, ck, ws.data_ptr() if n else None, n, st))
+        return gq, gk, gwq, gwk
 
     return on(device, stream, (q, k, dq_out, dk_out, table, table_k, q_weight, k_weight), run)
