@@ -72,12 +72,14 @@ static int encode_heads(CUtensorMap* m, const void* ptr, int B, int N, int H, in
   return r == CUDA_SUCCESS ? VSA_OK : VSA_ERR_CUDA;
 }
 
-// How a forward call is run: few rows a key/value head (at most kWsMaxRows)
-// take the step kernel, others the tcgen05 kernel; either splits its keys
-// when its CTAs are too few, as far as the most keys that a row can see allow
-// (the lengths are on the device).
+// How a forward call is run: few rows a key/value head (at most kWsMaxRows: 16
+// queries of 4 heads against 16384 keys, 2 x 8 key/value heads, 91 us, where
+// the tcgen05 kernel would give each head a CTA of 256 rows for its 16) take
+// the step kernel, others the tcgen05 kernel; either splits its keys when its
+// CTAs are too few, as far as the most keys that a row can see allow (the
+// lengths are on the device).
 constexpr int kWsMaxRows = 64;
-constexpr int kWfFixed = 6;
+constexpr int kWfFixed = 6;              // what a CTA of the tcgen05 kernel costs besides its blocks, in blocks
 // CTAs that a step call asks for, two an SM: with splits joined in a cluster 1.5
 // rounds of them (64 row tiles of 16384 keys: 5 splits 127 us, 7 95 us, 8 94 us,
 // 18 and a second kernel 104 us; 256 tiles of 2048: 2 splits 51 us, 8 84 us), with
@@ -199,10 +201,12 @@ static DkvSplit dkv_split(const WinArgs& a) {
   const long long all = (a.Nq + kWbRows - 1) / kWbRows;
   const long long seen = std::min(all, (std::min(1ll * a.window * a.unit, 1ll << 32) + a.unit + kWbRows) / kWbRows + 1);
   const long long wh = all * a.group, wn = seen * a.group;             // blocks that a key block is walked with
-  const long long sum = (s.heavy * wh + (s.blocks - s.heavy) * wn) * a.B * a.Hkv;
-  const long long share = std::max<long long>(kWbLeast, (sum + 148 * kWbShares - 1) / (148 * kWbShares));
-  s.sh = static_cast<int>(std::min<long long>(kWbMost, std::max(1ll, (wh + share - 1) / share)));
-  s.sn = static_cast<int>(std::min<long long>(kWbMost, std::max(1ll, (wn + share - 1) / share)));
+  // (in 64-bit floats: the product of the largest extents passes 63 bits)
+  const double sum = (1.0 * s.heavy * wh + 1.0 * (s.blocks - s.heavy) * wn) * a.B * a.Hkv;
+  const double share = std::max<double>(kWbLeast, std::ceil(sum / (148 * kWbShares)));
+  auto parts = [&](long long walk) { return static_cast<int>(std::min<double>(kWbMost, std::max(1.0, std::ceil(walk / share)))); };
+  s.sh = parts(wh);
+  s.sn = parts(wn);
   return s;
 }
 

@@ -28,12 +28,15 @@
 // blocks, 2048 of MMA).  So at d = 128 they take turns (window_wan5b 592 -> 540
 // us; at d = 64, where the products are half as long, turns cost 4 %).
 // window_wan5b, 6 heads of 27280 tokens, 8 frames and a sink: 540 us in bursts
-// (1070 TFLOP/s, 66 % of the measured peak), 550 us under the power cap.
+// (1070 TFLOP/s, 66 % of the measured peak), 550-610 us under the power cap.
 // Measured and not taken: a warpgroup on each half of a block's keys (four
 // softmax warps a sub-partition, row maxima joined by an OR barrier) 8 %
 // slower; 1/8 to 3/8 of the exponentials on the FMA pipe 2 to 10 % slower; the
 // maximum before any exponential, P released in halves and the next S issued
 // after a K wait 8 % slower; at d = 64 one slot a CTA and two CTAs an SM equal.
+// Short windows at d = 64 (window_tokens, 165 us): of 38k clk a CTA 4.3k pass
+// until the first scores, 2.5k a block, 1-2k more in each masked or first
+// block, 4k from the last P to the end, 1.7k to the next CTA.
 //
 // Rounding: P is rounded to the 16-bit input type for the P V MMA (its sum l
 // is taken from the float32 values), O once at the end.
@@ -52,6 +55,7 @@ constexpr int kWfKeys = 128;             // keys a block
 constexpr int kWfRegSoftmax = 208, kWfRegOther = 88;
 static_assert(2 * 128 * kWfRegSoftmax + 128 * kWfRegOther <= kWfThreads * 168, "register split over the launch budget");
 constexpr float kWfRescaleLog2 = 8.0f;
+
 template <int D>
 struct WfSmem {
   static constexpr int kSlab = 128 * 128;              // 128 rows x 64 channels
