@@ -77,21 +77,19 @@ struct DkvSplit {
   __host__ __device__ int tiles() const { return (sh > 1 ? heavy * sh : 0) + (sn > 1 ? (blocks - heavy) * sn : 0); }
 };
 
-// Stages an O-shaped tile of this thread's row (128 columns of TMEM at t, D of
-// them) times f into `buf`, swizzled as the TMA boxes are.
+// Stages this thread's row (D columns of TMEM at t) times f into the 128-row
+// tile `buf`, swizzled as the TMA boxes are.
 template <int D, bool F16>
-__device__ __forceinline__ void stage_row(uint32_t t, uint32_t buf, int r, float f, bool zero) {
+__device__ __forceinline__ void stage_row(uint32_t t, uint32_t buf, int r, float f) {
 #pragma unroll
   for (int q4 = 0; q4 < D / 32; ++q4) {
     uint32_t ov[32];
-    if (!zero) {
-      tmem_ld32(t + 32u * q4, ov);
-      tmem_wait_ld();
-    }
+    tmem_ld32(t + 32u * q4, ov);
+    tmem_wait_ld();
     uint32_t pk[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e)
-      pk[e] = zero ? 0u : pack_elem2<F16>(__uint_as_float(ov[2 * e]) * f, __uint_as_float(ov[2 * e + 1]) * f);
+      pk[e] = pack_elem2<F16>(__uint_as_float(ov[2 * e]) * f, __uint_as_float(ov[2 * e + 1]) * f);
     const uint32_t at = buf + r * 128u + (q4 >> 1) * WbSmem<D>::kSlab;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -346,7 +344,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     tc_fence_after();
     if (w == 0) {
       if (n > 0) {
-        if (ok) stage_row<D, F16>(tDQ + lane_base, base + L::kOwn0, r, a.scale, false);
+        if (ok) stage_row<D, F16>(tDQ + lane_base, base + L::kOwn0, r, a.scale);
         fence_proxy_async_smem();
         named_bar_sync(2, 128);
         if (ok && r == 0) {
@@ -738,7 +736,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
                                          mbar_wait(bar(DK_OUT + 1), 0, abort_flag, a.err));
       tc_fence_after();
       const uint32_t buf = base + (w == 0 ? L::kOwn1 : L::kOwn0);
-      if (ok) stage_row<D, F16>((w == 0 ? tDV : tDK) + lane_base, buf, r, w == 0 ? 1.f : a.scale, false);
+      if (ok) stage_row<D, F16>((w == 0 ? tDV : tDK) + lane_base, buf, r, w == 0 ? 1.f : a.scale);
       fence_proxy_async_smem();
       named_bar_sync(1 + w, 128);
       if (ok && r == 0) {
