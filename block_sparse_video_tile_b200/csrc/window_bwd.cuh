@@ -15,7 +15,11 @@
 // with the exponential unit (1024 clk) next.  The elementwise warps work on
 // the block in two halves of 64 columns (a warpgroup each, thread = row), and
 // write their 16-bit operand over the scores it came from, so P and dS never
-// leave TMEM.
+// leave TMEM.  Measured (window_bwd_wan5b, 6 heads): dQ 674-690 us, dK/dV
+// 1013-1020 us in bursts, tensor pipe 68-70 % active.  Not taken: 1/8 to 3/8 of
+// the exponentials on the FMA pipe 0 to 5 % slower; P^T released in three parts
+// 0.6 % faster, not worth its code; a warp of its own for dV's first part 3 %
+// slower.
 //
 // Rounding: P and dS are rounded to the 16-bit type as MMA operands; scores,
 // dP, delta and the accumulators are float32; results are rounded once.
