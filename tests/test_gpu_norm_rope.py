@@ -50,6 +50,8 @@ CASES = [
     ((3, 5, 7), 2, 5, 2, 128, "f16", "bhnd", False, "f32", (0, 0, 0), None),
     ((2, 9, 11), 1, 24, 24, 64, "bf16", "bhnd", False, None, (0, 3, 4), None),
     ((2, 9, 11), 3, 7, 1, 64, "f16", "bnhd", True, "f32", (0, 0, 0), (32, 16, 16)),
+    ((2, 5, 9), 2, 17, 19, 64, "f16", "bnhd", True, "f32", (0, 0, 0), None),      # several heads of a token side by side
+    ((3, 4, 3), 1, 9, 13, 128, "bf16", "bnhd", False, "same", (0, 0, 0), None),
     ((257, 1, 1), 1, 4, 4, 128, "bf16", "bnhd", False, "same", (100000, 0, 0), (128, 0, 0)),
     ((4, 13, 21), 1, 13, 13, 128, "bf16", "bhnd", True, "f32", (0, 0, 0), (0, 64, 64)),
 ]
