@@ -81,7 +81,7 @@ static int encode_heads(CUtensorMap* m, const void* ptr, int B, int N, int H, in
 constexpr int kWsMaxRows = 64;
 constexpr int kWfFixed = 6;              // what a CTA of the tcgen05 kernel costs besides its blocks, in blocks
 // CTAs that a step call asks for, two an SM: with splits joined in a cluster 1.5
-// rounds of them (64 row tiles of 16384 keys: 5 splits 127 us, 7 95 us, 8 94 us,
+// rounds of them (64 row tiles of 16384 keys: 5 splits 127 us, 7 95 us, 8 90 us,
 // 18 and a second kernel 104 us; 256 tiles of 2048: 2 splits 51 us, 8 84 us), with
 // the second kernel one round (8 tiles of 65536: 51 us, two rounds 56 us).
 constexpr int kWsClusterCtas = 148 * 3, kWsSplitCtas = 148 * 2;
@@ -104,8 +104,11 @@ static WinPlan win_plan(const WinArgs& a) {
   if (p.step) {
     const long long ctas = 1ll * a.B * a.Hkv * ((rows + kWsRows - 1) / kWsRows);
     const long long most = std::max(1ll, keys_of(a.Nq) / (kWsKeys * kWsWarps * 2));   // two tiles a warp at least
-    const long long want = std::min((kWsClusterCtas + ctas - 1) / ctas, most);
+    long long want = std::min((kWsClusterCtas + ctas - 1) / ctas, most);
     p.cluster = want <= kWsCluster;
+    // one split more if it leaves less of the last round of CTAs empty
+    auto used = [&](long long s) { return 1.0 * ctas * s / (148 * 2 * ((ctas * s + 295) / 296)); };
+    if (want < kWsCluster && want < most && used(want + 1) > used(want)) ++want;
     p.splits = static_cast<int>(std::max(1ll, p.cluster ? want : std::min({(kWsSplitCtas + ctas - 1) / ctas, most, 256ll})));
     if (p.splits == 1) p.cluster = false;
   } else {
