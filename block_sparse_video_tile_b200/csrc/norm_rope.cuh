@@ -351,7 +351,9 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_kernel(const __grid_c
           }
           const float r = rsqrtf(ss * (1.f / D) + a.eps);
           const uint64_t rc = f2_dup(live_row ? r : 0.f), r2 = f2_dup(r);
-          const uint64_t k2 = f2_dup(-r * r * r * (hx * (1.f / D)));                   // dx = r h - x r^3 mean(h x)
+          // dx = r h - x k, k = r^3 mean(h x): r is brought against hx first, since
+          // r^3 alone leaves float32 for rows below 1e-13 or above 1e13
+          const uint64_t k2 = f2_dup(-(r * hx * (1.f / D)) * r * r);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             da[e] = f2_fma(tx[e], rc, da[e]);
