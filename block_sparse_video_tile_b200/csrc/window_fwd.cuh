@@ -444,8 +444,9 @@ __global__ void __launch_bounds__(kWfThreads, 1)
     if (ok && n > 0)       // (a slot without blocks: Q has landed, so that it cannot overwrite the staged zeros)
       ok = __all_sync(0xffffffffu, mbar_wait(bar(c > 0 ? WB_O + s : WB_Q), 0, abort_flag, a.err));
     tc_fence_after();
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+    // (l = 0: the row sees nothing; a NaN among what it sees stays one)
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
     const size_t row = (static_cast<size_t>(b) * a.Hq + h) * a.Nq + i;
     const size_t rows = static_cast<size_t>(a.B) * a.Hq * a.Nq;
     if (n > 0 && splits == 1) {
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(kWfThreads, 1)
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            pk[e] = l > 0.f ? pack_elem2<F16>(__uint_as_float(ov[2 * e]) * inv, __uint_as_float(ov[2 * e + 1]) * inv) : 0u;
+            pk[e] = l == 0.f ? 0u : pack_elem2<F16>(__uint_as_float(ov[2 * e]) * inv, __uint_as_float(ov[2 * e + 1]) * inv);
           const uint32_t at = orow + (q4 >> 1) * L::kSlab;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__(kWfThreads, 1)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (l > 0.f)
+            if (l != 0.f)
               f = make_float4(__uint_as_float(ov[4 * e]) * inv, __uint_as_float(ov[4 * e + 1]) * inv,
                               __uint_as_float(ov[4 * e + 2]) * inv, __uint_as_float(ov[4 * e + 3]) * inv);
             reinterpret_cast<float4*>(op + 32 * q4)[e] = f;
@@ -534,16 +535,15 @@ __global__ void __launch_bounds__(256) window_combine_kernel(const __grid_consta
   for (int s = lane; s < splits; s += 32) mx = fmaxf(mx, ls[s * rows]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (mx == -INFINITY) mx = 0.f;                        // (no split sees anything, or one holds a NaN)
   float acc[D / 32] = {}, sum = 0.f;
-  if (mx != -INFINITY) {
 #pragma unroll 4
-    for (int s = warp; s < splits; s += W) {
-      const float w = exp2f((ls[s * rows] - mx) * 1.4426950408889634f);
-      sum += w;
-      const float* op = part + (s * rows + row) * D + lane;
+  for (int s = warp; s < splits; s += W) {
+    const float w = exp2f((ls[s * rows] - mx) * 1.4426950408889634f);
+    sum += w;
+    const float* op = part + (s * rows + row) * D + lane;
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(w, op[32 * e], acc[e]);
-    }
+    for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(w, op[32 * e], acc[e]);
   }
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) so[warp][lane + 32 * e] = acc[e];
@@ -558,13 +558,13 @@ __global__ void __launch_bounds__(256) window_combine_kernel(const __grid_consta
     x += so[k][2 * threadIdx.x];
     y += so[k][2 * threadIdx.x + 1];
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int i = static_cast<int>(row % a.Nq);
   const size_t bh = row / a.Nq;
   const int h = static_cast<int>(bh % a.Hq), b = static_cast<int>(bh / a.Hq);
   reinterpret_cast<uint32_t*>(a.out + b * a.os[0] + i * a.os[1] + h * a.os[2])[threadIdx.x] =
       pack_elem2<F16>(x * inv, y * inv);
-  if (threadIdx.x == 0) a.lse[row] = sum > 0.f ? mx + logf(sum) : -INFINITY;
+  if (threadIdx.x == 0) a.lse[row] = sum == 0.f ? -INFINITY : mx + logf(sum);
 }
 
 }  // namespace vsa

@@ -318,8 +318,9 @@ __global__ void __launch_bounds__(kWsThreads) window_step_kernel(const __grid_co
     cluster_sync();                                               // nobody leaves while its rows are read
   }
   if (!write) return;
-  const float inv = lt > 0.f ? 1.f / lt : 0.f;
-  const float lse = lt > 0.f ? (mt + log2f(lt)) * 0.69314718055994530942f : -INFINITY;
+  // (lt = 0: the row sees nothing; a NaN among what it sees stays one)
+  const float inv = lt == 0.f ? 0.f : 1.f / lt;
+  const float lse = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * 0.69314718055994530942f;
   const int i = r / a.group, h = hk * a.group + r % a.group;
   const size_t row = (static_cast<size_t>(b) * a.Hq + h) * a.Nq + i, rows = static_cast<size_t>(a.B) * a.Hq * a.Nq;
   const bool partial = !CLUSTER && splits > 1;

@@ -82,8 +82,9 @@ def window_attn(q, k, v, window: int, *, sink: int = 0, unit: int = 1, kv_len=No
     q: [B, Hq, Nq, d], k and v: [B, Hkv, Nk, d] (or the "bnhd" order), views with contiguous channels; Hq a multiple
     of Hkv.  kv_len: keys held of each sequence (device int32 [B], or an int; default Nk); rows behind it may hold
     anything.  q_start: position of the first query (default kv_len - Nq: the queries are the last tokens).  A query
-    that sees nothing gets O = 0 and LSE = -inf.  O is like q, LSE float32 [B, Hq, Nq]; both can be given, apart from
-    the inputs."""
+    that sees nothing gets O = 0 and LSE = -inf.  What some query sees must be finite (a NaN there makes the rows that
+    see it NaN, and may make others NaN too).  O is like q, LSE float32 [B, Hq, Nq]; both can be given, apart from the
+    inputs."""
     t, oshape, _, scale, size = _plan(q, k, v, window, sink, unit, layout, scale)
     device, B, Nk = q.device, t.B, t.Nk
     if out is not None or lse is not None:

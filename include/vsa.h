@@ -360,7 +360,8 @@ typedef struct vsa_window {
  * Scores, softmax and sums in float32.  workspace as for the other calls (0
  * bytes: may be NULL).  Any keys and queries that a mask leaves out
  * altogether (rows at kv_len and after, queries that see nothing) may hold
- * NaN or infinities; the others must be finite. */
+ * NaN or infinities; the others must be finite (a NaN there makes the rows
+ * that see it NaN, and may make others NaN too). */
 size_t vsa_window_attn_workspace_bytes(const vsa_window* w);
 int vsa_window_attn(const vsa_window* w, const void* q, const void* k, const void* v, float softmax_scale, void* o,
                     float* lse, void* workspace, size_t workspace_bytes, void* stream);
