@@ -24,6 +24,11 @@ struct WinArgs {
   float *lse, *delta;        // [B, Hq, Nq]
   long long qs[3], ks[3], vs[3], os[3], dos[3], dqs[3], dks[3], dvs[3];   // (b, n, h) strides, elements
   float scale, scale_log2;   // softmax_scale, softmax_scale * log2(e)
+  // fp16 gradient: [B, Hkv] largest bound on |dP - delta| (float bits), and
+  // [B, Hkv, chunks] largest |V_j|^2
+  unsigned int* grad_bound;
+  float* v_norms;
+  int chunks;
   unsigned int* err;
 };
 
@@ -56,6 +61,19 @@ __device__ __forceinline__ RowVis row_vis(const WinArgs& a, int len, int p) {
   r.lo = static_cast<int>(lo);
   r.first = static_cast<int>(first);
   return r;
+}
+
+// The query rows [lo, hi) that see a key; nobody: lo >= hi.
+struct KeyVis {
+  int lo, hi;
+};
+
+__device__ __forceinline__ KeyVis key_vis(const WinArgs& a, int len, int start, int key) {
+  if (key >= len) return KeyVis{0, 0};
+  const long long u = key / a.unit, p0 = u * a.unit;
+  const long long p1 = key < a.sink_tok ? (1ll << 40) : (u + a.window) * a.unit;
+  const long long Nq = a.Nq;
+  return KeyVis{static_cast<int>(min(max(p0 - start, 0ll), Nq)), static_cast<int>(min(max(p1 - start, 0ll), Nq))};
 }
 
 }  // namespace vsa

@@ -23,6 +23,18 @@
 //
 // Rounding: P and dS are rounded to the 16-bit type as MMA operands; scores,
 // dP, delta and the accumulators are float32; results are rounded once.
+//
+// fp16 holds 2^-14 .. 2^16 in full precision, and P is about one over the
+// number of keys, dS smaller still by dO: unscaled, thousands of keys and dO of
+// 1e-3 left dQ with 1.6 % of error in place of 0.1 %, and dO of 1e5 with
+// infinities.  So the fp16 kernels carry P times 2^12 (P <= 1), and dS times a
+// power of two f that brings a bound on it to 2^14 .. 2^15:
+//   |P (dP - delta)| <= |dO_i| max_j |V_j| + |delta_i| =: b_i.
+// dQ's f is its row's own; dK sums over queries, so its f is that of the
+// largest b_i of the key/value head, which the dQ kernel leaves behind (a
+// maximum, the same in any order).  |V_j| comes from window_v_norm_kernel.  The
+// factors leave with the results' scale, at no cost in the loops.  What fp16
+// still rounds away of a dS is 2^-25 / f, 2^-39 of the bound.
 #pragma once
 
 #include <cuda.h>
@@ -47,7 +59,7 @@ struct WbSmem {
   static constexpr int kBar = kB + kBSt * kBuf;
   static constexpr int kNumBars = 24;
   static constexpr int kMisc = kBar + kNumBars * 8;
-  static constexpr int kXch = kMisc + 16;              // dq: float [128], delta between the warpgroups
+  static constexpr int kXch = kMisc + 16;              // dq: float [2][128], delta and |dO|^2 between the warpgroups
   static constexpr int kStats = kXch;                  // dkv: (-lse * log2 e, -delta) of the walked queries,
                                                        // float [2 stages][2][128]
   static constexpr int kEnd = kStats + 2048;
@@ -100,6 +112,72 @@ __device__ __forceinline__ void stage_row(uint32_t t, uint32_t buf, int r, float
       st_shared_v4(at + static_cast<uint32_t>(((q4 & 1) * 4 + e) ^ (r & 7)) * 16u, pk[4 * e], pk[4 * e + 1],
                    pk[4 * e + 2], pk[4 * e + 3]);
   }
+}
+
+// ------------------------------------------------------------------ range of fp16 operands
+constexpr float kWbP = 4096.f;           // P's factor in the fp16 dK/dV kernel (log2: 12)
+
+// The largest |V_j|^2 of a key/value head's chunk of keys that some query sees
+// (the others may hold anything); sets the head's bound to 0 for the dQ kernel.
+// Reads V once, D / 8 lanes a row, 4 rows in flight a lane (window_bwd_tokens: 3.3 us
+// of latency; the whole gradient 139.6 us without the factors, 145.0 with).
+template <int D>
+__global__ void __launch_bounds__(256) window_v_norm_kernel(const __grid_constant__ WinArgs a) {
+  constexpr int LPR = D / 8, R = 256 / LPR, U = 4;
+  __shared__ float most[8];
+  const int hk = blockIdx.y, b = blockIdx.z, len = win_len(a, b), start = win_start(a, b, len);
+  const int j1 = static_cast<int>(1ll * a.Nk * (blockIdx.x + 1) / a.chunks);
+  const uint16_t* v = a.v + b * a.vs[0] + hk * a.vs[2] + threadIdx.x % LPR * 8;
+  // every CTA is resident from here on: the dQ kernel may set up beside them
+  asm volatile("griddepcontrol.launch_dependents;");
+  float m = 0.f;
+  for (int j0 = static_cast<int>(1ll * a.Nk * blockIdx.x / a.chunks); j0 < j1; j0 += U * R) {
+    uint4 x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * R + static_cast<int>(threadIdx.x) / LPR;
+      x[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (j >= j1) continue;
+      const KeyVis kv = key_vis(a, len, start, j);
+      if (kv.lo < kv.hi) x[u] = __ldg(reinterpret_cast<const uint4*>(v + j * a.vs[1]));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = unpack_elem2<true>(w[e]);
+        s = fmaf(f.x, f.x, fmaf(f.y, f.y, s));
+      }
+#pragma unroll
+      for (int o = 1; o < LPR; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      m = fmaxf(m, s);
+    }
+  }
+#pragma unroll
+  for (int o = LPR; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (threadIdx.x % 32 == 0) most[threadIdx.x / 32] = m;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = fmaxf(m, most[i]);
+  const size_t head = static_cast<size_t>(b) * a.Hkv + hk;
+  a.v_norms[head * a.chunks + blockIdx.x] = m;
+  if (blockIdx.x == 0) a.grad_bound[head] = 0u;
+}
+
+// A lane's share of the largest |V_j|^2 of a key/value head.
+__device__ __forceinline__ float lane_v_norm(const WinArgs& a, size_t head, int lane) {
+  float m = 0.f;
+  for (int c = lane; c < a.chunks; c += 32) m = fmaxf(m, a.v_norms[head * a.chunks + c]);
+  return m;
+}
+
+// The power of two that brings a bound to [2^14, 2^15); 1 for 0, infinities and NaN.
+__device__ __forceinline__ float grad_factor(unsigned int bound) {
+  if (bound == 0u || bound >= 0x7f800000u) return 1.f;
+  return __uint_as_float(static_cast<unsigned int>(min(268 - static_cast<int>(bound >> 23), 253)) << 23);
 }
 
 // ------------------------------------------------------------------ dQ
@@ -246,8 +324,8 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     const int i = i0 + r;
     const uint32_t lane_base = static_cast<uint32_t>((warp % 4) * 32) << 16;
     RowVis vis{0, 0, 0};
-    float lse2 = 0.f, delta = 0.f;
-    const size_t row = (static_cast<size_t>(b) * a.Hq + h) * a.Nq + i;
+    float lse2 = 0.f, delta = 0.f, g2 = 0.f;           // g2: |dO_i|^2 (fp16)
+    const size_t row = (static_cast<size_t>(b) * a.Hq + h) * a.Nq + i, head = static_cast<size_t>(b) * a.Hkv + hk;
     if (i < a.Nq) {
       vis = row_vis(a, len, start + i);
       const float ls = a.lse[row];
@@ -263,22 +341,42 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         for (int u = 0; u < 4; ++u) {
           const float2 xf = unpack_elem2<F16>(xs[u]), gf = unpack_elem2<F16>(gs[u]);
           delta = fmaf(xf.x, gf.x, fmaf(xf.y, gf.y, delta));
+          if (F16) g2 = fmaf(gf.x, gf.x, fmaf(gf.y, gf.y, g2));
         }
       }
     }
     float* xch = reinterpret_cast<float*>(sp + L::kXch);
-    if (w == 1) xch[r] = delta;
+    if (w == 1) {
+      xch[r] = delta;
+      if (F16) xch[128 + r] = g2;
+    }
     named_bar_sync(1, 256);
-    const float other = xch[r];
-    if (w == 0) delta += other;
-    named_bar_sync(1, 256);
-    if (w == 0) xch[r] = delta;
+    if (w == 0) {
+      delta += xch[r];
+      xch[r] = delta;
+      if (F16) xch[128 + r] = g2 += xch[128 + r];
+    }
     named_bar_sync(1, 256);
     delta = xch[r];
     if (w == 0 && i < a.Nq) a.delta[row] = delta;
+    float f = 1.f;                                     // dS's factor
+    if (F16) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");           // for window_v_norm_kernel's results
+      float v2 = lane_v_norm(a, head, lane);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) v2 = fmaxf(v2, __shfl_xor_sync(0xffffffffu, v2, o));
+      const unsigned int bound = __float_as_uint(sqrtf(xch[128 + r] * v2) + fabsf(delta));
+      f = grad_factor(bound);
+      if (w == 0) {
+        const bool sees = vis.hi > vis.lo || vis.first > 0;        // (a query that sees nothing may hold anything)
+        const unsigned int most = __reduce_max_sync(0xffffffffu, sees ? bound : 0u);
+        if (lane == 0) atomicMax(a.grad_bound + head, most);
+      }
+    }
 
     bool ok = true;
-    const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2), nl2 = f2_pack(-lse2, -lse2), nd2 = f2_pack(-delta, -delta);
+    const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2), nl2 = f2_pack(-lse2, -lse2), f2 = f2_pack(f, f),
+                   nd2 = f2_pack(-delta * f, -delta * f);
     for (int j = 0; j < n; ++j) {
       const int c0 = wb.block(j) * kWfKeys, sb = j & 1;
       const uint32_t tS = tmem + lane_base + 128u * sb + 64u * w, tP = tDP + lane_base + 64u * w;
@@ -324,7 +422,8 @@ __global__ void __launch_bounds__(kWbThreads, 1)
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
         float d0, d1;
-        f2_unpack(f2_add(f2_pack(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1])), nd2), d0, d1);
+        const uint64_t dp = f2_pack(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1]));
+        f2_unpack(F16 ? f2_fma(dp, f2, nd2) : f2_add(dp, nd2), d0, d1);
         x[2 * e] = __float_as_uint(__uint_as_float(x[2 * e]) * d0);
         x[2 * e + 1] = __float_as_uint(__uint_as_float(x[2 * e + 1]) * d1);
       }
@@ -348,7 +447,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     tc_fence_after();
     if (w == 0) {
       if (n > 0) {
-        if (ok) stage_row<D, F16>(tDQ + lane_base, base + L::kOwn0, r, a.scale);
+        if (ok) stage_row<D, F16>(tDQ + lane_base, base + L::kOwn0, r, a.scale / f);
         fence_proxy_async_smem();
         named_bar_sync(2, 128);
         if (ok && r == 0) {
@@ -417,6 +516,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
   }
   const int c0 = blk * kWbRows;
   const int len = win_len(a, b), start = win_start(a, b, len);
+  const float fds = F16 ? grad_factor(a.grad_bound[static_cast<size_t>(b) * a.Hkv + hk]) : 1.f;      // dS's factor
   // queries that see some key of [c0, c1): one range of rows, [qlo, qhi)
   int qb0 = 0, nq = 0;
   if (c0 < len) {
@@ -503,8 +603,8 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         break;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        stats[st * 256 + 32 * e + lane] = ls[e] == -INFINITY ? 0.f : -ls[e] * 1.4426950408889634f;
-        stats[st * 256 + 128 + 32 * e + lane] = -de[e];
+        stats[st * 256 + 32 * e + lane] = (ls[e] == -INFINITY ? 0.f : -ls[e] * 1.4426950408889634f) + (F16 ? 12.f : 0.f);
+        stats[st * 256 + 128 + 32 * e + lane] = F16 ? -de[e] * (fds / kWbP) : -de[e];
       }
       mbar_arrive(bar(DK_ST_FULL + st));
       if (++qi == nq) { qi = 0; ++h; }
@@ -598,16 +698,11 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const uint32_t tSw = tS + lane_base + 64u * w, tPw = tDP + lane_base + 64u * w;
     // the query rows that see this key: [qlo, qhi)
-    int qlo = 0, qhi = 0;
-    if (key < len) {
-      const int u = key / a.unit;
-      const long long p0 = static_cast<long long>(u) * a.unit;
-      const long long p1 = key < a.sink_tok ? (1ll << 40) : (static_cast<long long>(u) + a.window) * a.unit;
-      qlo = static_cast<int>(min(max(p0 - start, 0ll), static_cast<long long>(a.Nq)));
-      qhi = static_cast<int>(min(max(p1 - start, 0ll), static_cast<long long>(a.Nq)));
-    }
+    const KeyVis rows = key_vis(a, len, start, key);
+    const int qlo = rows.lo, qhi = rows.hi;
     bool ok = true;
-    const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2);
+    const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2), fd2 = f2_pack(fds / kWbP, fds / kWbP);
+    const float fo = w == 0 ? (F16 ? 1.f / kWbP : 1.f) : a.scale / fds;        // of dV, of dK
     int qi = q_first;
     for (int j = 0; j < n; ++j) {
       const int st = j & 1, i0 = (qb0 + qi) * kWbRows;
@@ -693,8 +788,10 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       for (int e = 0; e < 16; ++e) {
         const float4 d4 = nd[e];
         float d0, d1, d2, d3;
-        f2_unpack(f2_add(f2_pack(__uint_as_float(g[4 * e]), __uint_as_float(g[4 * e + 1])), f2_pack(d4.x, d4.y)), d0, d1);
-        f2_unpack(f2_add(f2_pack(__uint_as_float(g[4 * e + 2]), __uint_as_float(g[4 * e + 3])), f2_pack(d4.z, d4.w)), d2, d3);
+        const uint64_t dpa = f2_pack(__uint_as_float(g[4 * e]), __uint_as_float(g[4 * e + 1]));
+        const uint64_t dpb = f2_pack(__uint_as_float(g[4 * e + 2]), __uint_as_float(g[4 * e + 3]));
+        f2_unpack(F16 ? f2_fma(dpa, fd2, f2_pack(d4.x, d4.y)) : f2_add(dpa, f2_pack(d4.x, d4.y)), d0, d1);
+        f2_unpack(F16 ? f2_fma(dpb, fd2, f2_pack(d4.z, d4.w)) : f2_add(dpb, f2_pack(d4.z, d4.w)), d2, d3);
         if (masked) {                                  // (P is 0 there, but dP may not be finite)
           const uint32_t mm = (e < 8 ? m0 : m1) >> ((4 * e) & 31);
           if (!(mm & 1u)) d0 = 0.f;
@@ -740,7 +837,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
                                          mbar_wait(bar(DK_OUT + 1), 0, abort_flag, a.err));
       tc_fence_after();
       const uint32_t buf = base + (w == 0 ? L::kOwn1 : L::kOwn0);
-      if (ok) stage_row<D, F16>((w == 0 ? tDV : tDK) + lane_base, buf, r, w == 0 ? 1.f : a.scale);
+      if (ok) stage_row<D, F16>((w == 0 ? tDV : tDK) + lane_base, buf, r, fo);
       fence_proxy_async_smem();
       named_bar_sync(1 + w, 128);
       if (ok && r == 0) {
@@ -788,7 +885,8 @@ __global__ void __launch_bounds__(256) window_dkv_sum_kernel(const __grid_consta
   const int e = is_v ? at - 128 * D / 4 : at;
   const int key = blk * kWbRows + e / (D / 4), ch = (e % (D / 4)) * 4;
   if (key >= a.Nk) return;
-  const float f = is_v ? 1.f : a.scale;
+  const float f = !F16 ? (is_v ? 1.f : a.scale)
+                       : is_v ? 1.f / kWbP : a.scale / grad_factor(a.grad_bound[static_cast<size_t>(b) * a.Hkv + hk]);
   uint16_t* o = is_v ? a.dv + b * a.dvs[0] + key * a.dvs[1] + hk * a.dvs[2] : a.dk + b * a.dks[0] + key * a.dks[1] + hk * a.dks[2];
   *reinterpret_cast<uint2*>(o + ch) = make_uint2(pack_elem2<F16>(s.x * f, s.y * f), pack_elem2<F16>(s.z * f, s.w * f));
 }
