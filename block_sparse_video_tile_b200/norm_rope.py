@@ -127,7 +127,8 @@ def qk_norm_rope(q, k, grid, *, table=None, table_k=None, q_weight=None, k_weigh
                 s = side[1]
                 head_tensor("out", y, (s[b], s[n], s[h], s[3]), layout, q.dtype, device)
         apart([("out", y) for y in out if y is not None],
-              [(n, x) for n, x in (("q", q), ("k", k), ("table", table), ("q_weight", q_weight), ("k_weight", k_weight))
+              [(n, x) for n, x in (("q", q), ("k", k), ("table", table), ("table_k", table_k), ("q_weight", q_weight),
+                                  ("k_weight", k_weight))
                if x is not None])
     def run(st):
         sq, sk = sides

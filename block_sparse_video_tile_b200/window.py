@@ -93,7 +93,9 @@ def window_attn(q, k, v, window: int, *, sink: int = 0, unit: int = 1, kv_len=No
             head_tensor("out", out, (oshape[b], oshape[n], oshape[h], oshape[3]), layout, q.dtype, device)
         if lse is not None:
             _check_lse(lse, (B, t.Hq, t.Nq), device)
-        apart([(name, x) for name, x in (("out", out), ("lse", lse)) if x is not None], [("q", q), ("k", k), ("v", v)])
+        apart([(name, x) for name, x in (("out", out), ("lse", lse)) if x is not None],
+              [("q", q), ("k", k), ("v", v)] + [(name, x) for name, x in (("kv_len", kv_len), ("q_start", q_start))
+                                                if isinstance(x, torch.Tensor)])
     def run(st):
         n = _positions("kv_len", kv_len, 0, Nk, B, device)
         p0 = _positions("q_start", q_start, -_MAX_POS, _MAX_POS, B, device)
