@@ -92,6 +92,14 @@ def on(device, stream, tensors, run):
         return run(st)
 
 
+def spread(x, stream):
+    """A gradient as it is, or copied out (on the call's stream) where it was broadcast: o.sum().backward() gives one
+    value with strides of 0, which the kernels do not take."""
+    if x is None or 0 not in x.stride() or not x.is_cuda or all(s or n == 1 for s, n in zip(x.stride(), x.shape)):
+        return x
+    return on(x.device, stream, (x,), lambda st: x.contiguous())
+
+
 _F32 = {}
 
 

@@ -5,7 +5,7 @@ from __future__ import annotations
 import torch
 
 from ._native import VsaNormRope, VsaQkSide, check, lib
-from ._strided import AXES, DTYPES, Plans, apart, dims, empty_f32, head_tensor, on, sig, strides
+from ._strided import AXES, DTYPES, Plans, apart, dims, empty_f32, head_tensor, on, sig, spread, strides
 
 __all__ = ["rope_split", "rope_table", "qk_norm_rope", "qk_norm_rope_bwd"]
 
@@ -152,10 +152,12 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, grid, *, table=None, table_k=None, q_
                      eps: float = 1e-6, split=None, grid_k=None, interleaved: bool = True, layout: str = "bhnd",
                      stream=None):
     """Gradient of qk_norm_rope: (dq, dk, dq_weight, dk_weight) from the gradients of its results and its inputs.
-    The weights' gradients are float32 [d], None where the weight is None, summed in a fixed order."""
+    The weights' gradients are float32 [d], None where the weight is None, summed in a fixed order.  Broadcast gradients
+    (strides of 0) are copied first."""
     grid = tuple(grid)
     if (k is None) != (dk_out is None):
         raise ValueError("give k and dk_out, or neither")
+    dq_out, dk_out = spread(dq_out, stream), spread(dk_out, stream)
     args = (q, k, grid, grid if grid_k is None else tuple(grid_k), split, eps, interleaved, layout, table, table_k,
             q_weight, k_weight, (dq_out, dk_out))
     p, sides = _plan(_key(*args), *args)

@@ -7,7 +7,7 @@ import math
 import torch
 
 from ._native import VsaWindow, check, lib
-from ._strided import AXES, DTYPES, Plans, apart, dims, empty_f32, head_tensor, on, sig, strides
+from ._strided import AXES, DTYPES, Plans, apart, dims, empty_f32, head_tensor, on, sig, spread, strides
 
 __all__ = ["window_attn", "window_attn_bwd"]
 
@@ -127,7 +127,9 @@ def window_attn_bwd(do, q, k, v, out, lse, window: int, *, sink: int = 0, unit: 
                     layout: str = "bhnd", scale=None, stream=None):
     """Gradient of window_attn: (dq, dk, dv) from the gradient of O, the inputs and the (O, LSE) that it gave, with
     the same window.  A key/value head's gradient is the sum over its query heads; keys that no query sees get
-    zeros.  Every sum has a fixed order (the same bits each time)."""
+    zeros.  Every sum has a fixed order (the same bits each time).  A broadcast gradient (strides of 0) is copied
+    first."""
+    do = spread(do, stream)
     t, oshape, kshape, scale, size = _plan(q, k, v, window, sink, unit, layout, scale, do, out, lse)
     device, B = q.device, t.B
     def run(st):

@@ -200,3 +200,10 @@ def test_python_calls_refuse_cpu_tensors_and_bad_arguments():
         api.window_attn(q[0], q, q, 4)
     with pytest.raises(ValueError, match="bfloat16 or float16"):
         api.window_attn(q.double(), q, q, 4)
+
+
+def test_only_broadcast_gradients_are_copied():
+    from block_sparse_video_tile_b200._strided import spread
+    x = torch.zeros(1, 1, 4, 8)
+    for same in (None, x, x.as_strided((1, 1, 4, 8), (0, 0, 8, 1)), x.expand(2, 3, 4, 8)):      # (a CPU tensor is refused later)
+        assert spread(same, None) is same
