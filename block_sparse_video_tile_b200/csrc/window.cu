@@ -209,7 +209,7 @@ static DkvSplit dkv_split(const WinArgs& a) {
   const double share = std::max<double>(kWbLeast, std::ceil(sum / (148 * kWbShares)));
   auto parts = [&](long long walk) { return static_cast<int>(std::min<double>(kWbMost, std::max(1.0, std::ceil(walk / share)))); };
   s.sh = parts(wh);
-  s.sn = parts(wn);
+  s.sn = parts(wn);                                    // (wn <= wh: sn <= sh)
   return s;
 }
 
@@ -271,7 +271,7 @@ static int launch_bwd(const WinArgs& a, const DkvSplit& ds, float* part, cudaStr
     window_dkv_kernel<D, F16, false><<<grid, kWbThreads, smem, st>>>(mq, mg, mk, mv, mdk, mdv, a, ds, part);
   if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
   if (ds.tiles() > 0) {
-    const int shared = ds.sn > 1 ? ds.blocks - (ds.sh > 1 ? 0 : ds.heavy) : ds.heavy;
+    const int shared = ds.sn > 1 ? ds.blocks : ds.heavy;
     window_dkv_sum_kernel<D, F16><<<dim3(shared * (D / 4), a.Hkv, a.B), 256, 0, st>>>(a, ds, part);
   }
   return cudaGetLastError() == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;

@@ -83,14 +83,14 @@ __device__ __forceinline__ bool wb_base(const WinArgs& a, uint32_t raw, uint32_t
 
 // How the queries that see a key block are shared out: the first `heavy` key
 // blocks (they hold first units, which every later query sees) among sh CTAs
-// each, the others among sn.  A block with several CTAs gets its sums as float32
+// each, the others among sn <= sh.  A block with several CTAs gets its sums as float32
 // partial tiles, [dK, dV][128 rows][D] a CTA, added in order by
 // window_dkv_sum_kernel.
 struct DkvSplit {
   int blocks, heavy, sh, sn;
   __host__ __device__ int ctas() const { return heavy * sh + (blocks - heavy) * sn; }
-  // partial tiles of one (batch, key/value head)
-  __host__ __device__ int tiles() const { return (sh > 1 ? heavy * sh : 0) + (sn > 1 ? (blocks - heavy) * sn : 0); }
+  // partial tiles of one (batch, key/value head): the first ones of its CTAs
+  __host__ __device__ int tiles() const { return sn > 1 ? ctas() : sh > 1 ? heavy * sh : 0; }
 };
 
 // Stages this thread's row (D columns of TMEM at t) times f into the 128-row
@@ -505,11 +505,10 @@ __global__ void __launch_bounds__(kWbThreads, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int hk = blockIdx.y, b = blockIdx.z;
   // first keys first: they may be seen by every query
-  int blk = blockIdx.x, S = 1, sp_i = 0, x = 0;        // S: CTAs of this key block (SHARED: some have several)
-  bool hv = false;
+  int blk = blockIdx.x, S = 1, sp_i = 0;               // S: CTAs of this key block (SHARED: some have several)
   if (SHARED) {
-    x = blockIdx.x - ds.heavy * ds.sh;
-    hv = x < 0;
+    const int x = blockIdx.x - ds.heavy * ds.sh;
+    const bool hv = x < 0;
     S = hv ? ds.sh : ds.sn;
     blk = hv ? blockIdx.x / S : ds.heavy + x / S;
     sp_i = hv ? blockIdx.x % S : x % S;
@@ -814,8 +813,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(bar(DK_OUT), 0, abort_flag, a.err) &&
                                          mbar_wait(bar(DK_OUT + 1), 0, abort_flag, a.err));
       tc_fence_after();
-      const int tile = hv ? blockIdx.x : (ds.sh > 1 ? ds.heavy * ds.sh : 0) + x;
-      float* op = part + ((static_cast<size_t>(b) * a.Hkv + hk) * ds.tiles() + tile) * (2 * 128 * D) +
+      float* op = part + ((static_cast<size_t>(b) * a.Hkv + hk) * ds.tiles() + blockIdx.x) * (2 * 128 * D) +
                   (w == 0 ? 128 * D : 0) + r * D;
 #pragma unroll
       for (int q4 = 0; q4 < D / 32; ++q4) {
@@ -867,12 +865,10 @@ __global__ void __launch_bounds__(kWbThreads, 1)
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) window_dkv_sum_kernel(const __grid_constant__ WinArgs a, const DkvSplit ds,
                                                              const float* part) {
-  const int first = ds.sh > 1 ? 0 : ds.heavy;           // first shared block
-  const int blk = first + blockIdx.x / (D / 4), hk = blockIdx.y, b = blockIdx.z;     // D / 4 CTAs of 256 a block: 2 x 128 x D / 4
+  const int blk = blockIdx.x / (D / 4), hk = blockIdx.y, b = blockIdx.z;     // D / 4 CTAs of 256 a block: 2 x 128 x D / 4
   const bool hv = blk < ds.heavy;
   const int S = hv ? ds.sh : ds.sn;
-  if (S == 1) return;
-  const int tile = hv ? blk * S : (ds.sh > 1 ? ds.heavy * ds.sh : 0) + (blk - ds.heavy) * S;
+  const int tile = hv ? blk * S : ds.heavy * ds.sh + (blk - ds.heavy) * S;
   const int at = (blockIdx.x % (D / 4)) * 256 + threadIdx.x;                         // float4 of a tile
   const float4* p = reinterpret_cast<const float4*>(
                         part + ((static_cast<size_t>(b) * a.Hkv + hk) * ds.tiles() + tile) * (2 * 128 * D)) + at;
