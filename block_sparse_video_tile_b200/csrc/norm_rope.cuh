@@ -214,7 +214,7 @@ struct NrPlace {
 };
 
 // The (item, head) sequence of a lane's rows, kNrRows heads a step.  Every lane copies
-// (cp.async) exactly the 16-byte pieces that it reads later, kNrStages - 1 steps
+// (cp.async) exactly the 16-byte pieces that it reads later, nr_stages() - 1 steps
 // ahead and across items, so its ring needs no barrier and the loads in flight
 // do not depend on how many registers the arithmetic takes.
 template <int D, bool BWD>

@@ -72,18 +72,27 @@ static int encode_heads(CUtensorMap* m, const void* ptr, int B, int N, int H, in
   return r == CUDA_SUCCESS ? VSA_OK : VSA_ERR_CUDA;
 }
 
-// How a forward call is run: few rows a key/value head (at most kWsMaxRows: 16
-// queries of 4 heads against 16384 keys, 2 x 8 key/value heads, 91 us, where
-// the tcgen05 kernel would give each head a CTA of 256 rows for its 16) take
-// the step kernel, others the tcgen05 kernel; either splits its keys when its
-// CTAs are too few, as far as the most keys that a row can see allow (the
-// lengths are on the device).
+// How a forward call is run: few rows a key/value head take the step kernel,
+// others the tcgen05 kernel (which gives each query head of a group CTAs of its
+// own, however few its rows); either splits its keys when its CTAs are too few,
+// as far as the most keys that a row can see allow (the lengths are on the
+// device).  Where the two cross depends on the group; us of the step and of the
+// tcgen05 kernel, 16384 keys, d = 128:
+//   rows a key/value head     16        32        48        64        80        96
+//   2 x 8 heads, group 4    54 126    71 126    91 128    90 128   131 130   148 130
+//   8 x 8 heads, group 4   115 449   152 449   262 451   277 451   375 448   459 451
+//   2 x 8 heads, group 1    54  46    71  46    91  48    90  48   131  50   148  50
+//   2 x 24 heads, group 1  118  95   148  97   205  99   262 101   277 105   277 108
+// kWsMaxRows suits groups of 4 and more; it is late for a group of 1.
 constexpr int kWsMaxRows = 64;
 constexpr int kWfFixed = 6;              // what a CTA of the tcgen05 kernel costs besides its blocks, in blocks
 // CTAs that a step call asks for, two an SM: with splits joined in a cluster 1.5
 // rounds of them (64 row tiles of 16384 keys: 5 splits 127 us, 7 95 us, 8 90 us,
 // 18 and a second kernel 104 us; 256 tiles of 2048: 2 splits 51 us, 8 84 us), with
 // the second kernel one round (8 tiles of 65536: 51 us, two rounds 56 us).
+// Between them, where 1.5 rounds ask for 9 to 12 splits, a round and the second
+// kernel against 8 joined splits (32768 keys): 37 tiles 130 and 168 us, 40 tiles
+// 179 and 172, 48 tiles 202 and 174, 55 tiles 230 and 184.
 constexpr int kWsClusterCtas = 148 * 3, kWsSplitCtas = 148 * 2;
 
 struct WinPlan {

@@ -43,7 +43,8 @@ __device__ __forceinline__ int win_start(const WinArgs& a, int b, int len) {
 }
 
 // Position p sees [0, first) and [lo, hi); first <= lo (touching ranges are
-// joined into [0, hi) with first = 0); nothing: all 0.
+// joined into [0, hi) with first = 0); nothing: first = 0 and lo = hi (0 before
+// position 0, the length where the window begins behind the last key).
 struct RowVis {
   int first, lo, hi;
   __device__ __forceinline__ bool sees(int j) const { return j < hi && (j >= lo || j < first); }

@@ -1,12 +1,13 @@
 // window_step.cuh -- window attention of a few query rows against a long
 // cache (single new tokens, speculative tokens).
 //
-// Bound by HBM: every visible K and V row is read once for all the query
-// rows of its key/value head (2 * 2 * d bytes a key against 4 d flops a row:
-// 16 rows are still far below the balance of the legacy tensor path, and the
-// 128 rows of a tcgen05 tile would be nearly all padding).  So the rows --
-// the group's heads of each query token -- fill one m16 tile of mma.sync, and
-// the work is split over the keys: splits (CTAs) take contiguous runs of
+// Bound by HBM: every visible K and V row is read once for each tile of 16
+// query rows of its key/value head (2 * 2 * d bytes a key against 4 d flops a
+// row: 16 rows are still far below the balance of the legacy tensor path, and
+// the 128 rows of a tcgen05 tile would be nearly all padding).  So the rows --
+// the group's heads of each query token -- fill m16 tiles of mma.sync (one
+// for the usual call; further tiles read the keys again, from L2 where they
+// fit), and the work is split over the keys: splits (CTAs) take contiguous runs of
 // 16-key tiles, their four warps every fourth tile of the run.  A warp keeps
 // its own running maximum, sum and O and its own ring of kWsStages tiles
 // filled by cp.async (8 KB of K and V a tile at d = 128), so no warp waits for

@@ -49,8 +49,8 @@ _PLANS = Plans()
 
 
 def _plan(key, q, k, grid, grid_k, split, eps, interleaved, layout, table, table_k, q_weight, k_weight, dy):
-    """(vsa_norm_rope, for q and k (vsa_qk_side without addresses, shape of a result), backward workspace bytes) of
-    checked arguments.  dy: gradients of the results for the backward call, else None."""
+    """(vsa_norm_rope, [for q and for k: (vsa_qk_side without addresses, shape of a result)]) of checked arguments.
+    dy: gradients of the results for the backward call, else None."""
     plan = _PLANS.get(key)
     if plan is not None:
         return plan
@@ -114,7 +114,9 @@ def qk_norm_rope(q, k, grid, *, table=None, table_k=None, q_weight=None, k_weigh
     q, k: [B, H, N, d] or [B, N, H, d] views with contiguous channels (k may be None, and have its own batch, heads
     and grid).  table: rope_table(grid, d, ...), None for no rotation; table_k: the keys' (default: table, when the
     keys have the queries' grid).  q_weight, k_weight: [d], the type of q or float32; None for ones.  interleaved: a
-    pair is channels (2p, 2p + 1), else (p, p + d/2).  out: (q', k') to write to, apart from the inputs."""
+    pair is channels (2p, 2p + 1), else (p, p + d/2).  out: (q', k') to write to, apart from the inputs and each other
+    (from first to last byte: interleaved views of one buffer are refused).  The norm is over the d channels of each
+    head; a norm over all heads' channels together is not this call."""
     grid = tuple(grid)
     args = (q, k, grid, grid if grid_k is None else tuple(grid_k), split, eps, interleaved, layout, table, table_k,
             q_weight, k_weight, None)

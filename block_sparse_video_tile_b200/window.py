@@ -84,7 +84,7 @@ def window_attn(q, k, v, window: int, *, sink: int = 0, unit: int = 1, kv_len=No
     anything.  q_start: position of the first query (default kv_len - Nq: the queries are the last tokens).  A query
     that sees nothing gets O = 0 and LSE = -inf.  What some query sees must be finite (a NaN there makes the rows that
     see it NaN, and may make others NaN too).  O is like q, LSE float32 [B, Hq, Nq]; both can be given, apart from the
-    inputs."""
+    inputs and each other (from first to last byte)."""
     t, oshape, _, scale, size = _plan(q, k, v, window, sink, unit, layout, scale)
     device, B, Nk = q.device, t.B, t.Nk
     if out is not None or lse is not None:
