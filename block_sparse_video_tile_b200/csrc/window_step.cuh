@@ -28,6 +28,7 @@ constexpr int kWsKeys = 16;              // keys a tile
 constexpr int kWsRows = 16;              // query rows a CTA (token-major, then head of the group)
 constexpr int kWsStages = 3;
 constexpr int kWsCluster = 8;            // splits that are joined as one cluster
+constexpr float kWsUp = 15.f;            // fp16: P and l carry 2^kWsUp (P <= 1; why: see window_fwd.cuh)
 
 template <int D>
 struct WsSmem {
@@ -159,6 +160,7 @@ __global__ void __launch_bounds__(kWsThreads) window_step_kernel(const __grid_co
       q[kk][e] = p == nullptr ? 0u : *reinterpret_cast<const uint32_t*>(p + 16 * kk + 8 * (e >> 1) + 2 * (lane % 4));
     }
 
+  constexpr float kUp = F16 ? kWsUp : 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   float o[D / 8][4];
 #pragma unroll
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(kWsThreads) window_step_kernel(const __grid_co
       float sum = 0.f;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const float p0 = ex2_approx(s[t][2 * u] - mu), p1 = ex2_approx(s[t][2 * u + 1] - mu);
+        const float p0 = ex2_approx(s[t][2 * u] + (kUp - mu)), p1 = ex2_approx(s[t][2 * u + 1] + (kUp - mu));
         sum += p0 + p1;
         p[2 * t + u] = pack_elem2<F16>(p0, p1);                   // A fragment: rows u, keys 8 t ..
       }
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(kWsThreads) window_step_kernel(const __grid_co
   if (!write) return;
   // (lt = 0: the row sees nothing; a NaN among what it sees stays one)
   const float inv = lt == 0.f ? 0.f : 1.f / lt;
-  const float lse = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * 0.69314718055994530942f;
+  const float lse = lt == 0.f ? -INFINITY : (mt - kUp + log2f(lt)) * 0.69314718055994530942f;
   const int i = r / a.group, h = hk * a.group + r % a.group;
   const size_t row = (static_cast<size_t>(b) * a.Hq + h) * a.Nq + i, rows = static_cast<size_t>(a.B) * a.Hq * a.Nq;
   const bool partial = !CLUSTER && splits > 1;
