@@ -123,3 +123,42 @@ def test_gradients_of_zero_and_of_unseen_rows():
     o, lse = api.window_attn(q, k, v, 40, **kw)
     got = api.window_attn_bwd(do, q, k, v, o, lse, 40, **kw)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_captured_and_replayed_and_on_several_streams():
+    """The three or four launches of the fp16 gradient in two graphs that run at once, with inputs changed after the
+    capture, and eagerly on four streams."""
+    do, q, k, v = make(2, 4, 2, 700, 900, 64, 1e-2)
+    n = torch.tensor([900, 500], dtype=torch.int32, device="cuda")
+    kw = dict(sink=4, kv_len=n)
+
+    def both(**more):
+        o, lse = api.window_attn(q, k, v, 300, **kw, **more)
+        return (o, lse) + api.window_attn_bwd(do, q, k, v, o, lse, 300, **kw, **more)
+
+    want = both()
+    graphs = []
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            r = both()
+        graphs.append((gr, r))
+    do.mul_(64.0)
+    v.mul_(0.25)
+    n.copy_(torch.tensor([630, 899], dtype=torch.int32))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        graphs[0][0].replay()
+        with torch.cuda.stream(side):
+            graphs[1][0].replay()
+    torch.cuda.synchronize()
+    now = both()
+    assert not torch.equal(now[3], want[3])
+    for _, r in graphs:
+        assert all(torch.equal(a, b) for a, b in zip(r, now))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = [both(stream=streams[i % 4]) for i in range(16)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for r in got for a, b in zip(r, now))
